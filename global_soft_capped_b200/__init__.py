@@ -7,8 +7,12 @@ Two layers:
   ``g2attn_decode``, ``g2attn_decode_ring``, ``g2attn_decode_paged``,
   ``g2attn_decode_noalloc``, ``g2attn_backward_workspace_size``,
   ``g2attn_prefill_backward``, ``g2attn_varlen_backward_workspace_size``,
-  ``g2attn_prefill_varlen_backward``, ``g2attn_status_string``,
-  ``g2attn_get_device_error``,
+  ``g2attn_prefill_varlen_backward``, ``g2attn_rope``, ``g2attn_rope_append``,
+  ``g2attn_rope_append_ring``, ``g2attn_rope_append_paged``,
+  ``g2attn_extend_workspace_size``, ``g2attn_extend_paged``,
+  ``g2attn_pages_workspace_size``, ``g2attn_pages_grow``,
+  ``g2attn_pages_truncate``, ``g2attn_pages_fork``, ``g2attn_pages_compact``,
+  ``g2attn_pages_copy``, ``g2attn_status_string``, ``g2attn_get_device_error``,
   ``g2attn_selftest_wait_timeout``): plain argument marshalling of integers,
   floats and raw pointers through ctypes, returning the status code.
 * Tensor helpers (:func:`prefill`, :func:`prefill_varlen`, :func:`decode`,
@@ -23,7 +27,9 @@ first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libg2attn.so")
@@ -36,6 +42,7 @@ G2ATTN_ERR_CUDA = 4
 G2ATTN_ERR_DEVICE_TIMEOUT = 5
 G2ATTN_ERR_WORKSPACE = 6
 G2ATTN_ERR_CACHE_LEN = 7
+G2ATTN_ERR_CACHE_ROW = 8
 
 EXPORTS = (
     "g2attn_prefill",
@@ -50,6 +57,18 @@ EXPORTS = (
     "g2attn_prefill_backward",
     "g2attn_varlen_backward_workspace_size",
     "g2attn_prefill_varlen_backward",
+    "g2attn_rope",
+    "g2attn_rope_append",
+    "g2attn_rope_append_ring",
+    "g2attn_rope_append_paged",
+    "g2attn_extend_workspace_size",
+    "g2attn_extend_paged",
+    "g2attn_pages_workspace_size",
+    "g2attn_pages_grow",
+    "g2attn_pages_truncate",
+    "g2attn_pages_fork",
+    "g2attn_pages_compact",
+    "g2attn_pages_copy",
     "g2attn_status_string",
     "g2attn_get_device_error",
     "g2attn_selftest_wait_timeout",
@@ -100,6 +119,31 @@ def load_library():
     lib.g2attn_varlen_backward_workspace_size.restype = SZ
     lib.g2attn_prefill_varlen_backward.argtypes = [P] * 11 + [I] * 8 + [F, F, I, P, SZ, P]
     lib.g2attn_prefill_varlen_backward.restype = I
+    LL = ctypes.c_longlong
+    lib.g2attn_rope.argtypes = [P] * 6 + [I] * 6 + [F, I] + [LL] * 4 + [P]
+    lib.g2attn_rope.restype = I
+    lib.g2attn_rope_append.argtypes = [P] * 9 + [I] * 8 + [F] + [LL] * 3 + [P]
+    lib.g2attn_rope_append.restype = I
+    lib.g2attn_rope_append_ring.argtypes = [P] * 9 + [I] * 8 + [F] + [LL] * 3 + [P]
+    lib.g2attn_rope_append_ring.restype = I
+    lib.g2attn_rope_append_paged.argtypes = [P] * 10 + [I] * 10 + [F] + [LL] * 3 + [P]
+    lib.g2attn_rope_append_paged.restype = I
+    lib.g2attn_extend_workspace_size.argtypes = [I, I]
+    lib.g2attn_extend_workspace_size.restype = SZ
+    lib.g2attn_extend_paged.argtypes = [P] * 8 + [I] * 9 + [F, F, I, P, SZ, P]
+    lib.g2attn_extend_paged.restype = I
+    lib.g2attn_pages_workspace_size.argtypes = [I, I]
+    lib.g2attn_pages_workspace_size.restype = SZ
+    lib.g2attn_pages_grow.argtypes = [P] * 5 + [I] * 4 + [P, SZ, P]
+    lib.g2attn_pages_grow.restype = I
+    lib.g2attn_pages_truncate.argtypes = [P] * 4 + [I] * 4 + [P]
+    lib.g2attn_pages_truncate.restype = I
+    lib.g2attn_pages_fork.argtypes = [P] * 9 + [I] * 4 + [P, SZ, P]
+    lib.g2attn_pages_fork.restype = I
+    lib.g2attn_pages_compact.argtypes = [P] * 5 + [I] * 3 + [P, SZ, P]
+    lib.g2attn_pages_compact.restype = I
+    lib.g2attn_pages_copy.argtypes = [P, I, P, P, I, I, SZ, P]
+    lib.g2attn_pages_copy.restype = I
     lib.g2attn_status_string.argtypes = [I]
     lib.g2attn_status_string.restype = ctypes.c_char_p
     lib.g2attn_get_device_error.argtypes = []
@@ -197,6 +241,97 @@ def g2attn_decode_noalloc(q, k_cache, v_cache, cu_seqlens_k, out, lse, num_seqs,
     return load_library().g2attn_decode_noalloc(q, k_cache, v_cache, cu_seqlens_k, out, lse,
                                                 num_seqs, total_k, max_cache_len, H, Hkv, d,
                                                 query_scale, softcap, window, stream)
+
+
+def g2attn_rope(q, k, q_out, k_out, positions, freqs, num_tokens, H, Hkv, d, rotary_dim,
+                interleaved, mscale, inverse, q_stride, k_stride, q_out_stride, k_out_stride,
+                stream):
+    return load_library().g2attn_rope(q, k, q_out, k_out, positions, freqs, num_tokens, H, Hkv,
+                                      d, rotary_dim, interleaved, mscale, inverse, q_stride,
+                                      k_stride, q_out_stride, k_out_stride, stream)
+
+
+def g2attn_rope_append(q, k, v, q_out, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, freqs,
+                       num_seqs, total_q, total_k, H, Hkv, d, rotary_dim, interleaved, mscale,
+                       q_stride, k_stride, v_stride, stream):
+    return load_library().g2attn_rope_append(q, k, v, q_out, k_cache, v_cache, cu_seqlens_q,
+                                             cu_seqlens_k, freqs, num_seqs, total_q, total_k, H,
+                                             Hkv, d, rotary_dim, interleaved, mscale, q_stride,
+                                             k_stride, v_stride, stream)
+
+
+def g2attn_rope_append_ring(q, k, v, q_out, k_ring, v_ring, cu_seqlens_q, seq_lens, freqs,
+                            num_seqs, total_q, ring_size, H, Hkv, d, rotary_dim, interleaved,
+                            mscale, q_stride, k_stride, v_stride, stream):
+    return load_library().g2attn_rope_append_ring(q, k, v, q_out, k_ring, v_ring, cu_seqlens_q,
+                                                  seq_lens, freqs, num_seqs, total_q, ring_size,
+                                                  H, Hkv, d, rotary_dim, interleaved, mscale,
+                                                  q_stride, k_stride, v_stride, stream)
+
+
+def g2attn_rope_append_paged(q, k, v, q_out, k_blocks, v_blocks, cu_seqlens_q, block_table,
+                             seq_lens, freqs, num_seqs, total_q, num_blocks, block_size,
+                             max_blocks_per_seq, H, Hkv, d, rotary_dim, interleaved, mscale,
+                             q_stride, k_stride, v_stride, stream):
+    return load_library().g2attn_rope_append_paged(q, k, v, q_out, k_blocks, v_blocks,
+                                                   cu_seqlens_q, block_table, seq_lens, freqs,
+                                                   num_seqs, total_q, num_blocks, block_size,
+                                                   max_blocks_per_seq, H, Hkv, d, rotary_dim,
+                                                   interleaved, mscale, q_stride, k_stride,
+                                                   v_stride, stream)
+
+
+def g2attn_extend_workspace_size(max_T, d):
+    return load_library().g2attn_extend_workspace_size(max_T, d)
+
+
+def g2attn_extend_paged(q, k_blocks, v_blocks, out, lse, cu_seqlens_q, block_table, seq_lens,
+                        num_seqs, total_q, num_blocks, block_size, max_blocks_per_seq, max_T, H,
+                        Hkv, d, query_scale, softcap, window, workspace, workspace_bytes, stream):
+    return load_library().g2attn_extend_paged(q, k_blocks, v_blocks, out, lse, cu_seqlens_q,
+                                              block_table, seq_lens, num_seqs, total_q,
+                                              num_blocks, block_size, max_blocks_per_seq, max_T,
+                                              H, Hkv, d, query_scale, softcap, window, workspace,
+                                              workspace_bytes, stream)
+
+
+def g2attn_pages_workspace_size(num_seqs, num_blocks):
+    return load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
+
+
+def g2attn_pages_grow(block_table, seq_lens, ref_counts, add, granted, num_seqs, num_blocks,
+                      block_size, max_blocks_per_seq, workspace, workspace_bytes, stream):
+    return load_library().g2attn_pages_grow(block_table, seq_lens, ref_counts, add, granted,
+                                            num_seqs, num_blocks, block_size, max_blocks_per_seq,
+                                            workspace, workspace_bytes, stream)
+
+
+def g2attn_pages_truncate(block_table, seq_lens, ref_counts, keep, num_seqs, num_blocks,
+                          block_size, max_blocks_per_seq, stream):
+    return load_library().g2attn_pages_truncate(block_table, seq_lens, ref_counts, keep, num_seqs,
+                                                num_blocks, block_size, max_blocks_per_seq,
+                                                stream)
+
+
+def g2attn_pages_fork(block_table, seq_lens, parents, new_table, new_lens, ref_counts, copy_src,
+                      copy_dst, granted, num_seqs, num_blocks, block_size, max_blocks_per_seq,
+                      workspace, workspace_bytes, stream):
+    return load_library().g2attn_pages_fork(block_table, seq_lens, parents, new_table, new_lens,
+                                            ref_counts, copy_src, copy_dst, granted, num_seqs,
+                                            num_blocks, block_size, max_blocks_per_seq, workspace,
+                                            workspace_bytes, stream)
+
+
+def g2attn_pages_compact(block_table, ref_counts, copy_src, copy_dst, num_live, num_seqs,
+                         num_blocks, max_blocks_per_seq, workspace, workspace_bytes, stream):
+    return load_library().g2attn_pages_compact(block_table, ref_counts, copy_src, copy_dst,
+                                               num_live, num_seqs, num_blocks, max_blocks_per_seq,
+                                               workspace, workspace_bytes, stream)
+
+
+def g2attn_pages_copy(caches, num_caches, src, dst, num_pairs, num_blocks, page_bytes, stream):
+    return load_library().g2attn_pages_copy(caches, num_caches, src, dst, num_pairs, num_blocks,
+                                            page_bytes, stream)
 
 
 def g2attn_status_string(status):
@@ -428,3 +563,419 @@ def prefill_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens_k, 
     if st != G2ATTN_OK:
         raise G2AttnError(st, "g2attn_prefill_paged")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, cache appends, chunk attention, pages
+# ---------------------------------------------------------------------------
+class RopePlan(NamedTuple):
+    """What the rotary calls need besides the tensors: made once by :func:`rope_plan`."""
+    freqs: object        # int64 CUDA tensor (rotary_dim / 2): turns per position * 2^64
+    rotary_dim: int
+    interleaved: bool = False
+    mscale: float = 1.0
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained_len=8192,
+                     fast_turns=32.0, slow_turns=1.0):
+    """Radians per position of every pair, and the factor on the rotation.
+
+    w_i = base^(-2 i / rotary_dim), then for a context ``factor`` times the
+    trained one, ``scaling``: None; "linear", w_i / factor; "ntk", the base times
+    factor^(rotary_dim / (rotary_dim - 2)); "yarn", w_i / factor for pairs that
+    turn less than ``slow_turns`` times over ``trained_len`` positions, w_i for
+    those that turn more than ``fast_turns`` times, a ramp between, and the
+    rotation times 0.1 ln(factor) + 1.
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    half, mscale = rotary_dim // 2, 1.0
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    inv = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+    if scaling == "linear":
+        inv = [w / factor for w in inv]
+    elif scaling == "yarn":
+        def pair(turns):  # the (fractional) pair that turns so often over trained_len
+            return (rotary_dim * math.log(trained_len / (turns * 2.0 * math.pi))
+                    / (2.0 * math.log(base)))
+        low = max(math.floor(pair(fast_turns)), 0)
+        high = min(math.ceil(pair(slow_turns)), rotary_dim - 1)
+        ramp = [min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(half)]
+        inv = [w / factor * r + w * (1.0 - r) for w, r in zip(inv, ramp)]
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return inv, mscale
+
+
+def rope_plan(rotary_dim, *, interleaved=False, device="cuda", frequencies=None, mscale=None,
+              **scaling):
+    """A :class:`RopePlan` on ``device`` from :func:`rope_frequencies` (whose
+    arguments ``scaling`` are) or from ``frequencies`` (radians per position)."""
+    import torch
+    m = 1.0
+    if frequencies is None:
+        frequencies, m = rope_frequencies(rotary_dim, **scaling)
+    elif scaling:
+        raise ValueError("give frequencies or their parameters, not both")
+    if len(frequencies) != rotary_dim // 2:
+        raise ValueError("one frequency per pair")
+    turns = [round(w / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for w in frequencies]
+    freqs = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64,
+                         device=device)
+    return RopePlan(freqs, int(rotary_dim), bool(interleaved), m if mscale is None else mscale)
+
+
+class _on:
+    """The device of a tensor made current for a call (nothing when it is)."""
+    __slots__ = ("want", "had")
+
+    def __init__(self, t):
+        self.want = t.device.index
+
+    def __enter__(self):
+        import torch
+        self.had = torch.cuda.current_device()
+        if self.had != self.want:
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.had != self.want:
+            import torch
+            torch.cuda.set_device(self.had)
+
+
+def _raw_stream(stream, device):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _heads(name, t, device=None):
+    """(token count, heads, d, elements between tokens) of a (..., heads, d)
+    bf16 CUDA tensor whose tokens are evenly spaced and whose heads are dense."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() not in (3, 4):
+        raise ValueError(f"{name}: expected a bf16 CUDA tensor (tokens, heads, d) or (B, T, heads, d)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on another device than the first tensor")
+    sh, st = t.shape, t.stride()
+    H, d = sh[-2], sh[-1]
+    n, step = sh[-3], st[-3]
+    if t.dim() == 4:
+        if sh[0] > 1 and n > 1 and st[0] != n * step:
+            raise ValueError(f"{name}: the tokens of the batch are not evenly spaced")
+        if n == 1:
+            step = st[0]
+        n *= sh[0]
+    if n == 1:
+        step = H * d
+    if st[-1] != 1 or (H > 1 and st[-2] != d):
+        raise ValueError(f"{name}: heads of a token must be dense")
+    return n, H, d, step
+
+
+def _ints(name, t, n, device, dtype=None):
+    import torch
+    if (t.dtype != (dtype or torch.int32) or t.device != device or not t.is_contiguous()
+            or (n is not None and t.numel() != n)):
+        raise ValueError(f"{name}: expected {'' if n is None else n} contiguous "
+                         f"{dtype or torch.int32} values on {device}")
+    return t.data_ptr()
+
+
+def _cache(name, t, like, shape):
+    import torch
+    if t.dtype != torch.bfloat16 or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous bf16 tensor on {like.device}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit {shape}")
+    return t.data_ptr()
+
+
+def _plan_args(plan, device):
+    import torch
+    return _ints("plan.freqs", plan.freqs, plan.rotary_dim // 2, device, torch.int64)
+
+
+def _rope(q, k, positions, plan, inverse, out, stream):
+    import torch
+    n, H, d, qs = _heads("q", q)
+    nk, Hkv, dk, ks = _heads("k", k, q.device)
+    if nk != n or dk != d:
+        raise ValueError("q and k differ in tokens or head size")
+    if out is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        qos, kos = H * d, Hkv * d
+    else:
+        qo, ko = out
+        if qo.shape != q.shape or ko.shape != k.shape:
+            raise ValueError("out: expected the shapes of q and k")
+        qos, kos = _heads("out q", qo, q.device)[3], _heads("out k", ko, q.device)[3]
+    with _on(q):
+        st = load_library().g2attn_rope(
+            q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
+            _ints("positions", positions, n, q.device), _plan_args(plan, q.device), n, H, Hkv, d,
+            plan.rotary_dim, int(plan.interleaved), plan.mscale, inverse, qs, ks, qos, kos,
+            _raw_stream(stream, q.device))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_rope")
+    return qo, ko
+
+
+def rope(q, k, positions, plan, *, out=None, stream=None):
+    """Rotary positions: q (B,T,H,d) or (tokens,H,d), k alike with Hkv, either
+    of them a slice of a fused projection; positions int32 CUDA, one per token.
+    Returns rotated (q, k); ``out=(q, k)`` rotates in place."""
+    return _rope(q, k, positions, plan, 0, out, stream)
+
+
+def rope_backward(dq, dk, positions, plan, *, out=None, stream=None):
+    """Gradients of :func:`rope`: of its results in, of its inputs out."""
+    return _rope(dq, dk, positions, plan, 1, out, stream)
+
+
+def _append(where, q, k, v, cu_seqlens_q, num_seqs, q_out):
+    """Checks common to the appends: (sizes, strides, q_out, cu pointer)."""
+    import torch
+    n, H, d, qs = _heads("q", q)
+    nk, Hkv, dk, ks = _heads("k", k, q.device)
+    nv, Hv, dv, vs = _heads("v", v, q.device)
+    if (nk, dk) != (n, d) or (nv, Hv, dv) != (n, Hkv, d):
+        raise ValueError("q, k and v differ in tokens, heads or head size")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype != q.dtype \
+            or q_out.device != q.device:
+        raise ValueError("q_out: expected a contiguous bf16 tensor like q")
+    cu = None
+    if cu_seqlens_q is not None:
+        cu = _ints("cu_seqlens_q", cu_seqlens_q, num_seqs + 1, q.device)
+    elif n != num_seqs:
+        raise ValueError("without cu_seqlens_q every sequence has one token")
+    return n, H, Hkv, d, qs, ks, vs, q_out, cu
+
+
+def rope_append(q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, plan, *, q_out=None,
+                stream=None):
+    """Rotates q (returned) and k and writes k and v to the last rows of every
+    sequence of a packed cache (sum L,Hkv,d); cu_seqlens_q None: one token each."""
+    n_seqs = cu_seqlens_k.numel() - 1
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append", q, k, v, cu_seqlens_q, n_seqs,
+                                                  q_out)
+    kc = _cache("k_cache", k_cache, q, (None, Hkv, d))
+    vc = _cache("v_cache", v_cache, q, tuple(k_cache.shape))
+    with _on(q):
+        st = load_library().g2attn_rope_append(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+            _ints("cu_seqlens_k", cu_seqlens_k, None, q.device), _plan_args(plan, q.device),
+            n_seqs, n, k_cache.shape[0], H, Hkv, d, plan.rotary_dim, int(plan.interleaved),
+            plan.mscale, qs, ks, vs, _raw_stream(stream, q.device))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_rope_append")
+    return q_out
+
+
+def rope_append_ring(q, k, v, k_ring, v_ring, cu_seqlens_q, seq_lens, plan, *, q_out=None,
+                     stream=None):
+    """:func:`rope_append` into ring caches (n,R,Hkv,d); seq_lens with the new tokens."""
+    n_seqs = seq_lens.numel()
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append_ring", q, k, v, cu_seqlens_q,
+                                                  n_seqs, q_out)
+    kc = _cache("k_ring", k_ring, q, (n_seqs, None, Hkv, d))
+    vc = _cache("v_ring", v_ring, q, tuple(k_ring.shape))
+    with _on(q):
+        st = load_library().g2attn_rope_append_ring(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+            _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
+            k_ring.shape[1], H, Hkv, d, plan.rotary_dim, int(plan.interleaved), plan.mscale, qs,
+            ks, vs, _raw_stream(stream, q.device))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_rope_append_ring")
+    return q_out
+
+
+def rope_append_paged(q, k, v, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, plan, *,
+                      q_out=None, stream=None):
+    """:func:`rope_append` into paged caches (num_blocks,bs,Hkv,d); block_table
+    int32 (n, max_blocks), seq_lens with the new tokens."""
+    n_seqs = seq_lens.numel()
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append_paged", q, k, v, cu_seqlens_q,
+                                                  n_seqs, q_out)
+    kc = _cache("k_blocks", k_blocks, q, (None, None, Hkv, d))
+    vc = _cache("v_blocks", v_blocks, q, tuple(k_blocks.shape))
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+        raise ValueError("block_table: expected one row per sequence")
+    with _on(q):
+        st = load_library().g2attn_rope_append_paged(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+            _ints("block_table", block_table, None, q.device),
+            _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
+            k_blocks.shape[0], k_blocks.shape[1], block_table.shape[1], H, Hkv, d,
+            plan.rotary_dim, int(plan.interleaved), plan.mscale, qs, ks, vs,
+            _raw_stream(stream, q.device))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_rope_append_paged")
+    return q_out
+
+
+def extend_workspace(max_T, d, device="cuda"):
+    """A device buffer of g2attn_extend_workspace_size(max_T, d) bytes."""
+    import torch
+    return torch.empty(max(g2attn_extend_workspace_size(max_T, d), 16), dtype=torch.uint8,
+                       device=device)
+
+
+def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max_T, *,
+                 query_scale=1.0, softcap=50.0, window=0, out=None, lse=None, workspace=None,
+                 want_lse=True, stream=None):
+    """Attention of short chunks of new tokens, packed q (sum T,H,d), over paged
+    caches (num_blocks,bs,Hkv,d) that already hold them; seq_lens with the new
+    tokens. Returns (out (sum T,H,d), lse (H, sum T) | None)."""
+    import torch
+    if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
+        raise ValueError("q: expected a contiguous bf16 CUDA tensor (tokens, H, d)")
+    total_q, H, d = q.shape
+    kc = _cache("k_blocks", k_blocks, q, (None, None, None, d))
+    vc = _cache("v_blocks", v_blocks, q, tuple(k_blocks.shape))
+    n = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table: expected one row per sequence")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
+            or not out.is_contiguous():
+        raise ValueError("out: expected a contiguous bf16 tensor like q")
+    if lse is None and want_lse:
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.shape != (H, total_q) or lse.dtype != torch.float32
+                              or lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse: expected a contiguous fp32 tensor (H, tokens)")
+    if workspace is None:
+        workspace = extend_workspace(max_T, d, q.device)
+    with _on(q):
+        st = load_library().g2attn_extend_paged(
+            q.data_ptr(), kc, vc, out.data_ptr(), None if lse is None else lse.data_ptr(),
+            _ints("cu_seqlens_q", cu_seqlens_q, n + 1, q.device),
+            _ints("block_table", block_table, None, q.device),
+            _ints("seq_lens", seq_lens, None, q.device), n, total_q, k_blocks.shape[0],
+            k_blocks.shape[1], block_table.shape[1], int(max_T), H, k_blocks.shape[2], d,
+            query_scale, softcap, int(window), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _raw_stream(stream, q.device))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_extend_paged")
+    return out, lse
+
+
+def pages_workspace(num_seqs, num_blocks, device="cuda"):
+    """A device buffer of g2attn_pages_workspace_size(num_seqs, num_blocks) bytes."""
+    import torch
+    return torch.empty(max(g2attn_pages_workspace_size(num_seqs, num_blocks), 16),
+                       dtype=torch.uint8, device=device)
+
+
+def _table(block_table, ref_counts):
+    """(pointer, sequences, columns, pages, counts' pointer) of a page state."""
+    if not block_table.is_cuda or block_table.dim() != 2:
+        raise ValueError("block_table: expected an int32 CUDA tensor (num_seqs, max_blocks)")
+    dev = block_table.device
+    return (_ints("block_table", block_table, None, dev), block_table.shape[0],
+            block_table.shape[1], ref_counts.numel(), _ints("ref_counts", ref_counts, None, dev))
+
+
+def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, workspace=None,
+               stream=None):
+    """Lengthens every sequence by add rows with fresh pages, in place; returns
+    granted (num_seqs,) int32, 0 where the pages ran out."""
+    import torch
+    tp, n, cols, nb, rp = _table(block_table, ref_counts)
+    dev = block_table.device
+    granted = torch.empty(n, dtype=torch.int32, device=dev)
+    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    with _on(block_table):
+        st = load_library().g2attn_pages_grow(
+            tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev),
+            granted.data_ptr(), n, nb, int(block_size), cols, ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_pages_grow")
+    return granted
+
+
+def pages_truncate(block_table, seq_lens, ref_counts, keep, block_size, *, stream=None):
+    """Cuts every sequence to at most keep rows and gives its pages back, in place."""
+    tp, n, cols, nb, rp = _table(block_table, ref_counts)
+    dev = block_table.device
+    with _on(block_table):
+        st = load_library().g2attn_pages_truncate(
+            tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("keep", keep, n, dev), n, nb,
+            int(block_size), cols, _raw_stream(stream, dev))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_pages_truncate")
+
+
+def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, workspace=None,
+               stream=None):
+    """Every sequence s a fork of sequence parents[s] (s: stays). ref_counts in
+    place; returns (block_table, seq_lens, copy_src, copy_dst, granted), the
+    first two new. Copy the pages (:func:`pages_copy`) before appending."""
+    import torch
+    tp, n, cols, nb, rp = _table(block_table, ref_counts)
+    dev = block_table.device
+    table = torch.empty_like(block_table)
+    lens, src, dst, granted = torch.empty((4, n), dtype=torch.int32, device=dev).unbind(0)
+    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    with _on(block_table):
+        st = load_library().g2attn_pages_fork(
+            tp, _ints("seq_lens", seq_lens, n, dev), _ints("parents", parents, n, dev),
+            table.data_ptr(), lens.data_ptr(), rp, src.data_ptr(), dst.data_ptr(),
+            granted.data_ptr(), n, nb, int(block_size), cols, ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_pages_fork")
+    return table, lens, src, dst, granted
+
+
+def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
+    """Renumbers the live pages to the front of the cache, in place; returns
+    (copy_src, copy_dst, num_live) for :func:`pages_copy`."""
+    import torch
+    tp, n, cols, nb, rp = _table(block_table, ref_counts)
+    dev = block_table.device
+    src, dst = torch.empty((2, nb // 2), dtype=torch.int32, device=dev).unbind(0)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    with _on(block_table):
+        st = load_library().g2attn_pages_compact(
+            tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_pages_compact")
+    return src, dst, live
+
+
+def pages_copy(caches, src, dst, *, stream=None):
+    """Copies pages src to pages dst in every cache (num_blocks, ...) of a list
+    (K and V of all layers), all of one shape and type."""
+    caches = list(caches)
+    if not caches:
+        raise ValueError("caches: expected at least one tensor")
+    first = caches[0]
+    for c in caches:
+        if not c.is_cuda or c.device != first.device or c.shape != first.shape \
+                or c.dtype != first.dtype or not c.is_contiguous():
+            raise ValueError("caches: expected contiguous CUDA tensors of one shape and type")
+    dev, n = first.device, src.numel()
+    sp, dp = _ints("src", src, None, dev), _ints("dst", dst, n, dev)
+    if n == 0:
+        return
+    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    with _on(first):
+        st = load_library().g2attn_pages_copy(
+            ptrs, len(caches), sp, dp, n, first.shape[0],
+            first.numel() // first.shape[0] * first.element_size(), _raw_stream(stream, dev))
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, "g2attn_pages_copy")

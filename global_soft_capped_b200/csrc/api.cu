@@ -13,6 +13,9 @@
 #include "decode.cuh"
 #include "prefill_sm100.cuh"
 #include "backward_sm100.cuh"
+#include "extend.cuh"
+#include "pages.cuh"
+#include "rope.cuh"
 
 // Scratch of g2attn_decode_noalloc (see there): 24 MiB, reserved on every GPU
 // that loads the library until the process exits.
@@ -533,6 +536,180 @@ int launch_backward_varlen(const void* q, const void* k, const void* v, const vo
     return launch_bwd<D, g2::BW_Q>(m.q_q, m.o_q, m.k_q, m.v_q, P, static_cast<int>(q_ub), sms, st);
 }
 
+// ---------------------------------------------------------------------------
+// Rotary positions and cache appends
+// ---------------------------------------------------------------------------
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks and parameters that the rotation and the three appends share.
+int rope_common(g2::RopeParams& P, const void* q, const void* k, void* q_out, void* k_out,
+                const unsigned long long* freqs, int tokens, int H, int Hkv, int d, int rotary_dim,
+                float mscale, long long q_stride, long long k_stride) {
+    if (!q || !k || !q_out || !k_out || !freqs) return G2ATTN_ERR_INVALID_ARG;
+    if (tokens <= 0 || H <= 0 || Hkv <= 0 || rotary_dim <= 0 || rotary_dim > d || !finite_f(mscale))
+        return G2ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128 && d != 256) return G2ATTN_ERR_UNSUPPORTED;
+    if (rotary_dim % 16 != 0 || H > (1 << 20) || Hkv > (1 << 20)) return G2ATTN_ERR_UNSUPPORTED;
+    if (q_stride < static_cast<long long>(H) * d || k_stride < static_cast<long long>(Hkv) * d)
+        return G2ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || q_stride % 8 ||
+        k_stride % 8 || (reinterpret_cast<uintptr_t>(freqs) & 7u))
+        return G2ATTN_ERR_MISALIGNED;
+    P.q = static_cast<const __nv_bfloat16*>(q);
+    P.k = static_cast<const __nv_bfloat16*>(k);
+    P.q_out = static_cast<__nv_bfloat16*>(q_out);
+    P.k_out = static_cast<__nv_bfloat16*>(k_out);
+    P.freqs = freqs;
+    P.tokens = tokens;
+    P.H = H;
+    P.Hkv = Hkv;
+    P.rot = rotary_dim;
+    P.q_stride = q_stride;
+    P.k_stride = k_stride;
+    P.qo_stride = static_cast<long long>(H) * d;
+    P.mscale = mscale;
+    P.sign = 1.0f;
+    return G2ATTN_OK;
+}
+
+template <int D, int MODE>
+int launch_rope(g2::RopeParams& P, bool interleaved, cudaStream_t stream) {
+    constexpr int SL = D / 16;
+    const int heads = P.H + P.Hkv * (MODE == g2::ROPE_PLAIN ? 1 : 2);
+    const long long slots = static_cast<long long>(P.tokens) * SL;
+    // heads per thread: all the heads' work on one set of sines, but no fewer
+    // threads than fill the GPU
+    int hpg = 16;
+    while (hpg > 1 && slots * ((heads + hpg - 1) / hpg) < 148ll * 2048) hpg /= 2;
+    P.heads_per_group = hpg;
+    P.groups = (heads + hpg - 1) / hpg;
+    const long long blocks = (slots * P.groups + g2::ROPE_THREADS - 1) / g2::ROPE_THREADS;
+    if (blocks > INT32_MAX) return G2ATTN_ERR_UNSUPPORTED;
+    const int grid = static_cast<int>(blocks);
+    if (interleaved)
+        g2::rope_kernel<D, MODE, true><<<grid, g2::ROPE_THREADS, 0, stream>>>(P);
+    else
+        g2::rope_kernel<D, MODE, false><<<grid, g2::ROPE_THREADS, 0, stream>>>(P);
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+template <int MODE>
+int dispatch_rope(int d, g2::RopeParams& P, int interleaved, g2attn_stream_t stream) {
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    switch (d) {
+        case 64: return launch_rope<64, MODE>(P, interleaved != 0, st);
+        case 128: return launch_rope<128, MODE>(P, interleaved != 0, st);
+        case 256: return launch_rope<256, MODE>(P, interleaved != 0, st);
+        default: return G2ATTN_ERR_UNSUPPORTED;
+    }
+}
+
+// The appends' own arguments: v, its cache, and the sequences.
+int append_common(g2::RopeParams& P, const void* v, void* v_cache, const int* cu_seqlens_q,
+                  int num_seqs, int total_q, int Hkv, int d, long long v_stride) {
+    if (!v || !v_cache || num_seqs <= 0) return G2ATTN_ERR_INVALID_ARG;
+    if (!cu_seqlens_q && total_q != num_seqs) return G2ATTN_ERR_INVALID_ARG;
+    if (v_stride < static_cast<long long>(Hkv) * d) return G2ATTN_ERR_INVALID_ARG;
+    if (!aligned16(v) || !aligned16(v_cache) || v_stride % 8 || !aligned4(cu_seqlens_q))
+        return G2ATTN_ERR_MISALIGNED;
+    P.v = static_cast<const __nv_bfloat16*>(v);
+    P.v_out = static_cast<__nv_bfloat16*>(v_cache);
+    P.v_stride = v_stride;
+    P.cu_q = cu_seqlens_q;
+    P.num_seqs = num_seqs;
+    return G2ATTN_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Chunk attention over a paged cache
+// ---------------------------------------------------------------------------
+// Rows of a unit (2 heads x positions): the smallest of 16, 32 and 64 that holds
+// the longest chunk, so that short chunks keep more shared memory for K and V
+// in flight; longer chunks take several units.
+int extend_rows(int max_T) { return max_T <= 8 ? 16 : (max_T <= 16 ? 32 : 64); }
+
+size_t extend_ws_bytes(int max_T, int d) {
+    return 2ull * g2::EX_MAX_CTAS * extend_rows(max_T) * (static_cast<size_t>(d) + 4) * sizeof(float);
+}
+
+template <int D, int R, int SM>
+int launch_extend(g2::ExParams& P, cudaStream_t stream) {
+    using C = g2::ExCfg<D, R>;
+    const int sms = num_sms();
+    if (sms <= 0) return G2ATTN_ERR_CUDA;
+    auto kern = g2::extend_sm100<D, R, SM>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+        cudaSuccess)
+        return G2ATTN_ERR_CUDA;
+    const int grid = std::min(sms, g2::EX_MAX_CTAS);
+    kern<<<grid, g2::EX_THREADS, C::SMEM_BYTES, stream>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
+    if (grid == 1) return G2ATTN_OK;  // nothing to join
+    // the merge's prologue overlaps the attention kernel's end
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid - 1, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, g2::extend_merge<D, R>, static_cast<const g2::ExParams>(P), grid) !=
+        cudaSuccess)
+        return G2ATTN_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+template <int D, int R>
+int launch_extend_sm(g2::ExParams& P, bool fixed, cudaStream_t stream) {
+    return fixed ? launch_extend<D, R, g2::PF_SM_FIXED>(P, stream)
+                 : launch_extend<D, R, g2::PF_SM_CAP>(P, stream);
+}
+
+template <int D>
+int launch_extend_rows(int max_T, g2::ExParams& P, bool fixed, cudaStream_t stream) {
+    switch (extend_rows(max_T)) {
+        case 16: return launch_extend_sm<D, 16>(P, fixed, stream);
+        case 32: return launch_extend_sm<D, 32>(P, fixed, stream);
+        default: return launch_extend_sm<D, 64>(P, fixed, stream);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Pages
+// ---------------------------------------------------------------------------
+size_t pages_ws_bytes(int num_seqs, int num_blocks) {
+    const size_t a = (static_cast<size_t>(num_seqs) * sizeof(int) + 15) & ~static_cast<size_t>(15);
+    return a + static_cast<size_t>(num_blocks) * sizeof(int);
+}
+
+// Arguments that every call on tables has. `ws` is checked where `need_ws`.
+int pages_common(g2::PagesParams& P, const int* table, int* refs, int num_seqs, int num_blocks,
+                 int block_size, int max_blocks, bool need_ws, void* ws, size_t ws_bytes) {
+    if (!table || !refs) return G2ATTN_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || num_blocks <= 0 || max_blocks <= 0 || !pow2(block_size))
+        return G2ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_blocks) * block_size > INT32_MAX ||
+        static_cast<long long>(max_blocks) * block_size > INT32_MAX)
+        return G2ATTN_ERR_UNSUPPORTED;
+    if (!aligned4(table) || !aligned16(refs)) return G2ATTN_ERR_MISALIGNED;
+    if (need_ws) {
+        if (!ws || ws_bytes < pages_ws_bytes(num_seqs, num_blocks)) return G2ATTN_ERR_WORKSPACE;
+        if (!aligned16(ws)) return G2ATTN_ERR_MISALIGNED;
+        P.ws_base = static_cast<int*>(ws);
+        P.ws_pages = reinterpret_cast<int*>(static_cast<char*>(ws) +
+                                            (pages_ws_bytes(num_seqs, num_blocks) -
+                                             static_cast<size_t>(num_blocks) * sizeof(int)));
+    }
+    P.refs = refs;
+    P.num_seqs = num_seqs;
+    P.num_blocks = num_blocks;
+    P.block_shift = log2i(block_size);
+    P.max_blocks = max_blocks;
+    return G2ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -884,6 +1061,283 @@ int g2attn_decode_noalloc(const void* q, const void* k_cache, const void* v_cach
                          kNoAllocScratchBytes, stream);
 }
 
+int g2attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                const unsigned long long* freqs, int num_tokens, int H, int Hkv, int d,
+                int rotary_dim, int interleaved, float mscale, int inverse, long long q_stride,
+                long long k_stride, long long q_out_stride, long long k_out_stride,
+                g2attn_stream_t stream) {
+    g2::RopeParams P{};
+    if (!positions) return G2ATTN_ERR_INVALID_ARG;
+    int rc = rope_common(P, q, k, q_out, k_out, freqs, num_tokens, H, Hkv, d, rotary_dim, mscale,
+                         q_stride, k_stride);
+    if (rc) return rc;
+    if (q_out_stride < static_cast<long long>(H) * d ||
+        k_out_stride < static_cast<long long>(Hkv) * d)
+        return G2ATTN_ERR_INVALID_ARG;
+    // in place: every thread reads what it writes, so the rows must coincide
+    if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+        return G2ATTN_ERR_INVALID_ARG;
+    if (q_out_stride % 8 || k_out_stride % 8 || !aligned4(positions)) return G2ATTN_ERR_MISALIGNED;
+    P.positions = positions;
+    P.qo_stride = q_out_stride;
+    P.ko_stride = k_out_stride;
+    P.sign = inverse ? -1.0f : 1.0f;
+    return dispatch_rope<g2::ROPE_PLAIN>(d, P, interleaved, stream);
+}
+
+int g2attn_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                       void* v_cache, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                       const unsigned long long* freqs, int num_seqs, int total_q, int total_k,
+                       int H, int Hkv, int d, int rotary_dim, int interleaved, float mscale,
+                       long long q_stride, long long k_stride, long long v_stride,
+                       g2attn_stream_t stream) {
+    g2::RopeParams P{};
+    if (!cu_seqlens_k || total_k <= 0) return G2ATTN_ERR_INVALID_ARG;
+    int rc = rope_common(P, q, k, q_out, k_cache, freqs, total_q, H, Hkv, d, rotary_dim, mscale,
+                         q_stride, k_stride);
+    if (rc) return rc;
+    rc = append_common(P, v, v_cache, cu_seqlens_q, num_seqs, total_q, Hkv, d, v_stride);
+    if (rc) return rc;
+    if (q_out == q && q_stride != P.qo_stride) return G2ATTN_ERR_INVALID_ARG;
+    if (!aligned4(cu_seqlens_k)) return G2ATTN_ERR_MISALIGNED;
+    P.cu_k = cu_seqlens_k;
+    P.total_k = total_k;
+    return dispatch_rope<g2::ROPE_TO_LINEAR>(d, P, interleaved, stream);
+}
+
+int g2attn_rope_append_ring(const void* q, const void* k, const void* v, void* q_out, void* k_ring,
+                            void* v_ring, const int* cu_seqlens_q, const int* seq_lens,
+                            const unsigned long long* freqs, int num_seqs, int total_q,
+                            int ring_size, int H, int Hkv, int d, int rotary_dim, int interleaved,
+                            float mscale, long long q_stride, long long k_stride,
+                            long long v_stride, g2attn_stream_t stream) {
+    g2::RopeParams P{};
+    if (!seq_lens || !pow2(ring_size)) return G2ATTN_ERR_INVALID_ARG;
+    int rc = rope_common(P, q, k, q_out, k_ring, freqs, total_q, H, Hkv, d, rotary_dim, mscale,
+                         q_stride, k_stride);
+    if (rc) return rc;
+    rc = append_common(P, v, v_ring, cu_seqlens_q, num_seqs, total_q, Hkv, d, v_stride);
+    if (rc) return rc;
+    if (q_out == q && q_stride != P.qo_stride) return G2ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_seqs) * ring_size > INT32_MAX) return G2ATTN_ERR_UNSUPPORTED;
+    if (!aligned4(seq_lens)) return G2ATTN_ERR_MISALIGNED;
+    P.seq_lens = seq_lens;
+    P.ring_mask = ring_size - 1;
+    P.ring_shift = log2i(ring_size);
+    return dispatch_rope<g2::ROPE_TO_RING>(d, P, interleaved, stream);
+}
+
+int g2attn_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                             void* k_blocks, void* v_blocks, const int* cu_seqlens_q,
+                             const int* block_table, const int* seq_lens,
+                             const unsigned long long* freqs, int num_seqs, int total_q,
+                             int num_blocks, int block_size, int max_blocks_per_seq, int H,
+                             int Hkv, int d, int rotary_dim, int interleaved, float mscale,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             g2attn_stream_t stream) {
+    g2::RopeParams P{};
+    if (!block_table || !seq_lens || !pow2(block_size) || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0)
+        return G2ATTN_ERR_INVALID_ARG;
+    int rc = rope_common(P, q, k, q_out, k_blocks, freqs, total_q, H, Hkv, d, rotary_dim, mscale,
+                         q_stride, k_stride);
+    if (rc) return rc;
+    rc = append_common(P, v, v_blocks, cu_seqlens_q, num_seqs, total_q, Hkv, d, v_stride);
+    if (rc) return rc;
+    if (q_out == q && q_stride != P.qo_stride) return G2ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_blocks) * block_size > INT32_MAX ||
+        static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX)
+        return G2ATTN_ERR_UNSUPPORTED;
+    if (!aligned4(block_table) || !aligned4(seq_lens)) return G2ATTN_ERR_MISALIGNED;
+    P.block_table = block_table;
+    P.seq_lens = seq_lens;
+    P.block_shift = log2i(block_size);
+    P.max_blocks = max_blocks_per_seq;
+    P.num_blocks = num_blocks;
+    return dispatch_rope<g2::ROPE_TO_PAGED>(d, P, interleaved, stream);
+}
+
+size_t g2attn_extend_workspace_size(int max_T, int d) {
+    if (max_T <= 0 || (d != 64 && d != 128 && d != 256)) return 0;
+    return extend_ws_bytes(max_T, d);
+}
+
+int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                        float* lse, const int* cu_seqlens_q, const int* block_table,
+                        const int* seq_lens, int num_seqs, int total_q, int num_blocks,
+                        int block_size, int max_blocks_per_seq, int max_T, int H, int Hkv, int d,
+                        float query_scale, float softcap, int window, void* workspace,
+                        size_t workspace_bytes, g2attn_stream_t stream) {
+    if (!q || !k_blocks || !v_blocks || !out || !cu_seqlens_q || !block_table || !seq_lens)
+        return G2ATTN_ERR_INVALID_ARG;
+    if (num_seqs <= 0 || total_q <= 0 || max_T <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || !pow2(block_size))
+        return G2ATTN_ERR_INVALID_ARG;
+    int rc = check_common(H, Hkv, d, query_scale, softcap, window);
+    if (rc) return rc;
+    if (num_seqs > g2::EX_MAX_SEQS) return G2ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * block_size > INT32_MAX ||
+        static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX)
+        return G2ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_blocks) || !aligned16(v_blocks) || !aligned16(out) ||
+        (lse && !aligned16(lse)) || !aligned4(cu_seqlens_q) || !aligned4(block_table) ||
+        !aligned4(seq_lens))
+        return G2ATTN_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < extend_ws_bytes(max_T, d)) return G2ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return G2ATTN_ERR_MISALIGNED;
+    g2::ExParams P{};
+    P.q = static_cast<const __nv_bfloat16*>(q);
+    P.k = static_cast<const __nv_bfloat16*>(k_blocks);
+    P.v = static_cast<const __nv_bfloat16*>(v_blocks);
+    P.out = static_cast<__nv_bfloat16*>(out);
+    P.lse = lse;
+    P.cu_q = cu_seqlens_q;
+    P.table = block_table;
+    P.lens = seq_lens;
+    P.ws_s = static_cast<float*>(workspace);
+    P.ws_o = P.ws_s + 2ull * g2::EX_MAX_CTAS * extend_rows(max_T) * 4;
+    P.num_seqs = num_seqs;
+    P.total_q = total_q;
+    P.num_blocks = num_blocks;
+    P.block_shift = log2i(block_size);
+    P.max_blocks = max_blocks_per_seq;
+    P.H = H;
+    P.Hkv = Hkv;
+    P.window = window;
+    P.min_tiles = 1;
+    fill_cap(query_scale, softcap, P.k_exp, P.cap_l2, P.scale_l2, P.has_cap);
+    const bool fixed = P.has_cap && P.cap_l2 <= g2::PF_FIXED_REF_MAX;
+    P.fixed_ref = fixed ? P.cap_l2 - 64.0f : 0.f;
+    P.timeout_ns = wait_limit_ns();
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    switch (d) {
+        case 64: return launch_extend_rows<64>(max_T, P, fixed, st);
+        case 128: return launch_extend_rows<128>(max_T, P, fixed, st);
+        default: return launch_extend_rows<256>(max_T, P, fixed, st);
+    }
+}
+
+size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks) {
+    if (num_seqs <= 0 || num_blocks <= 0) return 0;
+    return pages_ws_bytes(num_seqs, num_blocks);
+}
+
+int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
+                      int* granted, int num_seqs, int num_blocks, int block_size,
+                      int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
+                      g2attn_stream_t stream) {
+    g2::PagesParams P{};
+    if (!seq_lens || !add || !granted) return G2ATTN_ERR_INVALID_ARG;
+    int rc = pages_common(P, block_table, ref_counts, num_seqs, num_blocks, block_size,
+                          max_blocks_per_seq, true, workspace, workspace_bytes);
+    if (rc) return rc;
+    if (!aligned4(seq_lens) || !aligned4(add) || !aligned4(granted)) return G2ATTN_ERR_MISALIGNED;
+    P.table = block_table;
+    P.lens = seq_lens;
+    P.arg = add;
+    P.granted = granted;
+    g2::pages_assign<false><<<1, g2::PG_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+int g2attn_pages_truncate(int* block_table, int* seq_lens, int* ref_counts, const int* keep,
+                          int num_seqs, int num_blocks, int block_size, int max_blocks_per_seq,
+                          g2attn_stream_t stream) {
+    g2::PagesParams P{};
+    if (!seq_lens || !keep) return G2ATTN_ERR_INVALID_ARG;
+    int rc = pages_common(P, block_table, ref_counts, num_seqs, num_blocks, block_size,
+                          max_blocks_per_seq, false, nullptr, 0);
+    if (rc) return rc;
+    if (!aligned4(seq_lens) || !aligned4(keep)) return G2ATTN_ERR_MISALIGNED;
+    P.table = block_table;
+    P.lens = seq_lens;
+    P.arg = keep;
+    g2::pages_truncate_rows<<<num_seqs / 4 + 1, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+int g2attn_pages_fork(const int* block_table, const int* seq_lens, const int* parents,
+                      int* new_table, int* new_lens, int* ref_counts, int* copy_src,
+                      int* copy_dst, int* granted, int num_seqs, int num_blocks, int block_size,
+                      int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
+                      g2attn_stream_t stream) {
+    g2::PagesParams P{};
+    if (!seq_lens || !parents || !new_table || !new_lens || !copy_src || !copy_dst || !granted)
+        return G2ATTN_ERR_INVALID_ARG;
+    if (new_table == block_table || new_lens == seq_lens) return G2ATTN_ERR_INVALID_ARG;
+    int rc = pages_common(P, block_table, ref_counts, num_seqs, num_blocks, block_size,
+                          max_blocks_per_seq, true, workspace, workspace_bytes);
+    if (rc) return rc;
+    if (!aligned4(seq_lens) || !aligned4(parents) || !aligned4(new_table) || !aligned4(new_lens) ||
+        !aligned4(copy_src) || !aligned4(copy_dst) || !aligned4(granted))
+        return G2ATTN_ERR_MISALIGNED;
+    P.table_in = block_table;
+    P.lens_in = seq_lens;
+    P.arg = parents;
+    P.table = new_table;
+    P.lens = new_lens;
+    P.src = copy_src;
+    P.dst = copy_dst;
+    P.granted = granted;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    g2::pages_assign<true><<<1, g2::PG_THREADS, 0, st>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
+    g2::pages_fork_rows<<<num_seqs, 128, 0, st>>>(P);
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+int g2attn_pages_compact(int* block_table, int* ref_counts, int* copy_src, int* copy_dst,
+                         int* num_live, int num_seqs, int num_blocks, int max_blocks_per_seq,
+                         void* workspace, size_t workspace_bytes, g2attn_stream_t stream) {
+    g2::PagesParams P{};
+    if (!num_live || (num_blocks > 1 && (!copy_src || !copy_dst))) return G2ATTN_ERR_INVALID_ARG;
+    int rc = pages_common(P, block_table, ref_counts, num_seqs, num_blocks, 1, max_blocks_per_seq,
+                          true, workspace, workspace_bytes);
+    if (rc) return rc;
+    if (!aligned4(copy_src) || !aligned4(copy_dst) || !aligned4(num_live))
+        return G2ATTN_ERR_MISALIGNED;
+    P.table = block_table;
+    P.src = copy_src;
+    P.dst = copy_dst;
+    P.num_live = num_live;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    g2::pages_plan<<<1, g2::PG_THREADS, 0, st>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
+    const long long blocks = (static_cast<long long>(num_seqs) * max_blocks_per_seq + 255) / 256;
+    g2::pages_remap<<<static_cast<int>(std::min(blocks, 2368ll)), 256, 0, st>>>(P);
+    return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
+}
+
+int g2attn_pages_copy(void* const* caches, int num_caches, const int* src, const int* dst,
+                      int num_pairs, int num_blocks, size_t page_bytes, g2attn_stream_t stream) {
+    if (!caches || !src || !dst || num_caches <= 0 || num_pairs <= 0 || num_blocks <= 0 ||
+        page_bytes == 0)
+        return G2ATTN_ERR_INVALID_ARG;
+    if (page_bytes % 16 != 0) return G2ATTN_ERR_UNSUPPORTED;
+    const unsigned long long chunks = (page_bytes + g2::PG_COPY_CHUNK - 1) / g2::PG_COPY_CHUNK;
+    if (chunks > INT32_MAX || chunks * num_pairs > INT32_MAX) return G2ATTN_ERR_UNSUPPORTED;
+    for (int i = 0; i < num_caches; ++i) {
+        if (!caches[i]) return G2ATTN_ERR_INVALID_ARG;
+        if (!aligned16(caches[i])) return G2ATTN_ERR_MISALIGNED;
+    }
+    if (!aligned4(src) || !aligned4(dst)) return G2ATTN_ERR_MISALIGNED;
+    for (int i = 0; i < num_caches; i += g2::PG_MAX_CACHES) {
+        g2::PagesCopyParams P{};
+        const int n = std::min(num_caches - i, g2::PG_MAX_CACHES);
+        for (int j = 0; j < n; ++j) P.caches[j] = caches[i + j];
+        P.src = src;
+        P.dst = dst;
+        P.num_pairs = num_pairs;
+        P.num_blocks = num_blocks;
+        P.chunks = static_cast<int>(chunks);
+        P.page_vecs = page_bytes / 16;
+        g2::pages_copy<<<dim3(P.chunks * num_pairs, n, 1), g2::PG_COPY_THREADS, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(P);
+        if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
+    }
+    return G2ATTN_OK;
+}
+
 const char* g2attn_status_string(int status) {
     switch (status) {
         case G2ATTN_OK: return "ok";
@@ -894,6 +1348,7 @@ const char* g2attn_status_string(int status) {
         case G2ATTN_ERR_DEVICE_TIMEOUT: return "device wait timed out";
         case G2ATTN_ERR_WORKSPACE: return "workspace missing or too small";
         case G2ATTN_ERR_CACHE_LEN: return "decode sequence longer than max_cache_len";
+        case G2ATTN_ERR_CACHE_ROW: return "appended token without a row in its cache";
         default: return "unknown status";
     }
 }
@@ -907,7 +1362,8 @@ int g2attn_get_device_error(void) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g2::g_device_error, &zero, sizeof(zero)) != cudaSuccess)
         return G2ATTN_ERR_CUDA;
-    return (v & g2::DEVERR_TIMEOUT) ? G2ATTN_ERR_DEVICE_TIMEOUT : G2ATTN_ERR_CACHE_LEN;
+    if (v & g2::DEVERR_TIMEOUT) return G2ATTN_ERR_DEVICE_TIMEOUT;
+    return (v & g2::DEVERR_CACHE_LEN) ? G2ATTN_ERR_CACHE_LEN : G2ATTN_ERR_CACHE_ROW;
 }
 
 int g2attn_selftest_wait_timeout(int timeout_us) {

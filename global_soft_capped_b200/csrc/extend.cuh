@@ -1,0 +1,849 @@
+// extend.cuh -- attention of a chunk of new tokens per sequence (1 .. some
+// tens) over a paged KV cache with pages of any power of two of rows, for
+// B200 / sm_100a.
+//
+// Operation: as the prefill of packed sequences, q_offset_s = S_s - T_s: query
+// i of sequence s sits at position p = S_s - T_s + i and sees keys j <= p, on a
+// local layer those with p - j < window; s_j = C tanh(x_j / C) (or x_j),
+// out = sum_j softmax_j(s) v_j, lse = ln sum_j exp(s_j).
+//
+// What bounds it: every visible K and V row is read once from HBM for all the
+// chunk's queries and both heads of its group; the products are small next to
+// that. So the matrix products are turned round: S^T = K Q^T has the 128 keys of a
+// tile as the rows M of the MMA and the chunk's rows (position, head) as its
+// columns N = R = 16, 32 or 64, and O^T = V^T P^T has the d columns as M. A
+// short chunk then costs no padding to 128 rows, every softmax thread owns
+// one key (a TMEM lane) for R/2 rows, and K and V are each read from shared
+// memory once per tile.
+//
+// Work split: units are (sequence, KV head, R/2 positions), each a run of
+// 128-key tiles. All tiles of the launch are numbered in one line and each CTA
+// takes an equal stretch of it, crossing from unit to unit without emptying
+// its pipeline, so that ragged lengths and few sequences load every SM alike.
+// A unit cut by a stretch's end leaves unnormalised partial results (O, max,
+// sums) in the workspace, at most two per CTA, and extend_merge joins them in
+// the order of the keys (no atomics: results do not depend on timing).
+//
+// One CTA of 416 threads per SM:
+//   warps 0..7   softmax: warpgroup w/4 takes rows w/4*R/2 .. of S^T, thread =
+//                key; writes P as bf16 into shared memory; at a unit's end
+//                reads O^T (lane = d column) and writes out or the partial.
+//   warp 8       tensor memory, one thread issues the UMMAs.
+//   warps 9..12  producers: 16-byte asynchronous copies of Q, K and V rows into
+//                128-byte-swizzled tiles. Each row's page is looked up, so
+//                pages may be of any size; rows behind the last visible key
+//                are filled with zeros (what the cache holds there, NaN
+//                included, does not matter).
+// Softmax: fp32, log2 domain, the fixed shift of the prefill when the cap
+// allows it, else a running max with lazy rescaling of O (when a max grows by
+// more than 2^8). P is rounded to bf16 for the product; out is
+// normalised by the sum of the rounded weights, lse uses the unrounded sum.
+#pragma once
+
+#include "common.cuh"
+#include "prefill_sm100.cuh"
+
+namespace g2 {
+
+constexpr int EX_BN = 128;            // keys per tile
+constexpr int EX_SM_THREADS = 256;    // softmax warps 0..7
+constexpr int EX_WARP_MMA = 8;
+constexpr int EX_WARP_PROD = 9;
+constexpr int EX_PROD_WARPS = 4;
+constexpr int EX_THREADS = 416;
+constexpr int EX_MAX_SEQS = 1024;     // per-launch table in shared memory
+constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
+constexpr float EX_RESCALE_LOG2 = 8.0f;
+
+template <int D, int R>
+struct ExCfg {
+    static constexpr int TQ = R / 2;                      // positions per unit
+    static constexpr int HC = R / 2;                      // rows per softmax warpgroup
+    static constexpr int SLOT_COLS = D < 128 ? D : 128;   // d columns of a slot
+    static constexpr int SLOT_BYTES = EX_BN * SLOT_COLS * 2;
+    static constexpr int KSL = D / SLOT_COLS;             // slots per K (or V) tile
+    static constexpr int NCH = SLOT_COLS / 64;            // 64-column chunks per slot
+    static constexpr int CH_BYTES = EX_BN * 128;          // 16 KB
+    static constexpr int Q_BYTES = R * D * 2;
+    static constexpr int QB = R * D <= 8192 ? 2 : 1;      // Q buffers
+    static constexpr int P_BYTES = R * EX_BN * 2;         // two buffers
+    static constexpr int FIXED = QB * Q_BYTES + 2 * P_BYTES;
+    // rows 64..127 of the d = 64 product read one chunk past their slot: the
+    // tiles after the ring must span that
+    static constexpr int PAD = D == 64 && FIXED < CH_BYTES ? CH_BYTES - FIXED : 0;
+    static constexpr int CUM_BYTES = 8 * (EX_MAX_SEQS + 1);
+    static constexpr int CTRL_BYTES = 256 + 2 * 2 * 4 * HC * 12;
+    static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - PAD - CUM_BYTES - CTRL_BYTES - 64;
+    static constexpr int NS_FIT = BUDGET / SLOT_BYTES;
+    static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
+    static constexpr int SMEM_BYTES =
+        1024 + NS * SLOT_BYTES + FIXED + PAD + CUM_BYTES + CTRL_BYTES + 64;
+    static constexpr int O_BLOCKS = D <= 128 ? 1 : D / 128;  // M = 128 blocks of O^T
+    static constexpr int TMEM_USED = 2 * R + O_BLOCKS * R;
+    static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : (TMEM_USED <= 128 ? 128 : 256);
+    static_assert(NS >= 2 * KSL && SMEM_BYTES <= 227 * 1024 && TMEM_USED <= 256, "budget");
+};
+
+struct ExParams {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* out;
+    float* lse;
+    const int* cu_q;
+    const int* table;
+    const int* lens;
+    float* ws_o;     // [2 * EX_MAX_CTAS][R][D]
+    float* ws_s;     // [2 * EX_MAX_CTAS][R][4]: max, fp32 sum, sum of rounded weights, unused
+    int num_seqs, total_q, num_blocks, block_shift, max_blocks;
+    int H, Hkv, window;
+    float k_exp, cap_l2, scale_l2, fixed_ref;
+    int has_cap;
+    int min_tiles;   // tiles a CTA takes at least
+    unsigned long long timeout_ns;
+};
+
+// A unit and its stretch of the line of tiles.
+struct ExUnit {
+    int seq, g, t0;      // first query row of the unit within its sequence
+    int tvalid;          // its query rows (1 .. TQ)
+    int qrow;            // packed row of query t0
+    int p0;              // position of query t0
+    int lo, hi;          // visible keys [lo, hi) of the whole unit
+    int tiles;
+    long long first;     // number of its first tile in the line
+};
+
+__device__ __forceinline__ int ex_len(const ExParams& P, int s) {
+    const long long cap = static_cast<long long>(P.max_blocks) << P.block_shift;
+    return static_cast<int>(max(0ll, min(static_cast<long long>(P.lens[s]), cap)));
+}
+
+// Visible keys and tiles (at least one, so that every unit writes its rows) of
+// positions p0 .. p0 + n - 1 of a sequence of length L.
+__device__ __forceinline__ int ex_range(int p0, int n, int L, int window, int& lo, int& hi) {
+    lo = window > 0 ? max(0, p0 - window + 1) : 0;
+    hi = min(max(0, p0 + n), L);
+    return max(1, (hi - lo + EX_BN - 1) / EX_BN);
+}
+
+template <int TQ>
+__device__ __forceinline__ long long ex_seq_tiles(const ExParams& P, int s) {
+    int qb, T;
+    pf_seq_rows(P.cu_q, s, P.total_q, &qb, &T);
+    const int L = ex_len(P, s);
+    long long n = 0;
+    for (int t = 0; t < T; t += TQ) {
+        int lo, hi;
+        n += ex_range(L - T + t, min(TQ, T - t), L, P.window, lo, hi);
+    }
+    return n * P.Hkv;
+}
+
+// cum[s] = tiles before sequence s, cum[num_seqs] = all. Whole CTA.
+template <int TQ>
+__device__ __forceinline__ void ex_cum(const ExParams& P, long long* cum) {
+    for (int s = threadIdx.x; s < P.num_seqs; s += blockDim.x) cum[s + 1] = ex_seq_tiles<TQ>(P, s);
+    if (threadIdx.x == 0) cum[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        long long base = 0;
+        for (int b = 1; b <= P.num_seqs; b += 32) {
+            const int i = b + threadIdx.x;
+            long long x = i <= P.num_seqs ? cum[i] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (static_cast<int>(threadIdx.x) >= o) x += y;
+            }
+            x += base;
+            if (i <= P.num_seqs) cum[i] = x;
+            base = __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// CTAs that take part: every one of them gets at least one tile.
+__device__ __forceinline__ long long ex_ctas(const ExParams& P, long long all, int grid) {
+    const long long n = (all + P.min_tiles - 1) / P.min_tiles;
+    return n < grid ? n : grid;
+}
+
+// First tile of CTA c's stretch, and the CTA that has a tile.
+__device__ __forceinline__ long long ex_start(long long c, long long all, long long ctas) {
+    return c * all / ctas;
+}
+__device__ __forceinline__ long long ex_owner(long long tile, long long all, long long ctas) {
+    return ((tile + 1) * ctas - 1) / all;
+}
+
+// The unit that holds tile `x` of the line.
+template <int TQ>
+__device__ __forceinline__ void ex_unit(const ExParams& P, const long long* cum, long long x,
+                                        ExUnit& U) {
+    int lo = 0, hi = P.num_seqs - 1;  // last s with cum[s] <= x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    U.seq = lo;
+    int qb, T;
+    pf_seq_rows(P.cu_q, lo, P.total_q, &qb, &T);
+    const int L = ex_len(P, lo);
+    const long long per_g = (cum[lo + 1] - cum[lo]) / P.Hkv;
+    long long rem = x - cum[lo];
+    U.g = static_cast<int>(rem / per_g);
+    rem -= U.g * per_g;
+    for (U.t0 = 0;; U.t0 += TQ) {
+        U.tvalid = min(TQ, T - U.t0);
+        U.p0 = L - T + U.t0;
+        U.tiles = ex_range(U.p0, U.tvalid, L, P.window, U.lo, U.hi);
+        if (rem < U.tiles || U.t0 + TQ >= T) break;
+        rem -= U.tiles;
+    }
+    U.first = x - rem;
+    U.qrow = qb + U.t0;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Shared-memory writes of this thread before, tensor-core reads after.
+__device__ __forceinline__ void fence_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// N = 8, 16 or 32 columns of this warp's 32 TMEM lanes; waits for the data.
+template <int N>
+__device__ __forceinline__ void ex_tmem_ld(uint32_t a, float (&f)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "columns");
+    uint32_t r[N];
+    if constexpr (N == 8) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7])
+            : "r"(a)
+            : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+            "%10, %11, %12, %13, %14, %15}, [%16];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(a)
+            : "memory");
+    } else {
+        tmem_ld32(a, r);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void ex_tmem_st(uint32_t a, const float (&f)[N]) {
+    uint32_t r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(f[i]);
+    if constexpr (N == 8) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+            : "memory");
+    } else if constexpr (N == 16) {
+        tmem_st16(a, r);
+    } else {
+        tmem_st32(a, r);
+    }
+}
+
+// Combines N values per lane over the 32 lanes of a warp (sum or max): halves the
+// columns of a lane with every exchange, so N + log2(32 / N) - 1 shuffles in
+// all. Lane l ends with column ex_col<N>(l) of the result.
+template <int N, bool MAX>
+__device__ __forceinline__ float ex_reduce(float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = N, o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i < n / 2) {
+                    const float send = up ? v[i] : v[i + n / 2];
+                    const float keep = up ? v[i + n / 2] : v[i];
+                    const float got = __shfl_xor_sync(0xffffffffu, send, o);
+                    v[i] = MAX ? fmaxf(keep, got) : keep + got;
+                }
+            }
+            n >>= 1;
+        } else {
+            const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+            v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+        }
+    }
+    return v[0];
+}
+template <int N>
+__device__ __forceinline__ int ex_col(int lane) {
+    return N == 32 ? lane : (N == 16 ? lane >> 1 : lane >> 2);
+}
+
+// SM = PF_SM_FIXED or PF_SM_CAP (any running max; has_cap tells the cap).
+template <int D, int R, int SM>
+__global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) {
+    using C = ExCfg<D, R>;
+    constexpr int HC = C::HC;
+    constexpr bool FIX = SM == PF_SM_FIXED;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* sSlots = smem;
+    unsigned char* sQ = sSlots + C::NS * C::SLOT_BYTES;
+    unsigned char* sP = sQ + C::QB * C::Q_BYTES;
+    unsigned char* ctrl = sP + 2 * C::P_BYTES + C::PAD;
+    long long* cum = reinterpret_cast<long long*>(ctrl);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl + ((C::CUM_BYTES + 63) / 64) * 64);
+    uint64_t* slot_full = bars;            // [8]
+    uint64_t* slot_empty = bars + 8;       // [8]
+    uint64_t* q_empty = bars + 16;         // [2]
+    uint64_t* s_full = bars + 18;          // [2]
+    uint64_t* p_full = bars + 20;          // [2]
+    uint64_t* p_empty = bars + 22;         // [2]
+    uint64_t* o_full = bars + 24;
+    uint64_t* wg_max = bars + 25;          // [2] warpgroup exchanges
+    uint64_t* wg_sum = bars + 27;          // [2]
+    uint64_t* drain = bars + 29;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 30);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 31);
+    // row statistics that the warps of a warpgroup exchange: maxima
+    // [tile parity][warpgroup][warp][HC], sums [unit parity][..][..][HC][2]
+    float* s_max = reinterpret_cast<float*>(bars + 32);
+    float* s_sum = s_max + 2 * 2 * 4 * HC;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t lim = P.timeout_ns;
+    if (tid == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&slot_full[i], EX_PROD_WARPS * 32);
+            mbar_init(&slot_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], EX_SM_THREADS);
+            mbar_init(&p_empty[i], 1);
+            mbar_init(&wg_max[i], 128);
+            mbar_init(&wg_sum[i], 128);
+        }
+        mbar_init(o_full, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == EX_WARP_MMA) {
+        tmem_alloc(tmem_ptr, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    ex_cum<C::TQ>(P, cum);  // ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = *tmem_ptr;
+    // the merge may be scheduled; it waits for this grid before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const long long all = cum[P.num_seqs];
+    const long long ctas = ex_ctas(P, all, gridDim.x);
+    long long x0 = 0, x1 = 0;
+    if (static_cast<long long>(blockIdx.x) < ctas) {
+        x0 = ex_start(blockIdx.x, all, ctas);
+        x1 = ex_start(blockIdx.x + 1ll, all, ctas);
+    }
+
+    if (warp >= EX_WARP_PROD) {
+        // -------------------------------------------------------- producers
+        const int pw = warp - EX_WARP_PROD;       // rows pw*32 .. of a tile
+        const int pt = tid - EX_WARP_PROD * 32;
+        uint32_t fill = 0, told = 0;              // slots filled, slots signalled
+        bool ok = true;
+        // copies of every filled slot have landed: hand them over
+        auto tell_to = [&](uint32_t upto) {
+            fence_async_smem();
+            for (; told < upto; ++told) mbar_arrive(&slot_full[told % C::NS]);
+        };
+        auto await = [&](uint64_t* bar, uint32_t parity) {
+            if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return;
+            cp_async_wait<0>();  // the consumer may need them before it frees this
+            tell_to(fill);
+            ok = mbar_wait(bar, parity, abort_flag, lim, SITE_EX_PROD);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        const long long rstride = static_cast<long long>(P.Hkv) * D;
+        // this lane's row of key tile `base`: its cache row, -1 outside [lo, hi)
+        auto row_of = [&](const ExUnit& U, int tile) -> int {
+            const int key = U.lo + tile * EX_BN + pw * 32 + lane;
+            if (key >= U.hi) return -1;
+            int b = P.table[static_cast<size_t>(U.seq) * P.max_blocks + (key >> P.block_shift)];
+            b = max(0, min(b, P.num_blocks - 1));
+            return (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
+        };
+        auto begin_slot = [&]() -> uint32_t {
+            const uint32_t s = fill % C::NS;
+            if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
+            return s;
+        };
+        auto end_slot = [&]() {
+            cp_async_commit();
+            ++fill;
+            if (fill - told >= static_cast<uint32_t>(C::NS - 1)) {
+                cp_async_wait<C::NS - 2>();
+                tell_to(fill - (C::NS - 2));
+            }
+        };
+        constexpr int LPR = C::SLOT_COLS / 8;  // lanes per row of a slot
+        constexpr int RPI = 32 / LPR;          // rows per instruction
+        auto load_tile = [&](const __nv_bfloat16* cache, int g, int rows, int s0) {
+            const int c = lane % LPR;
+            const uint32_t s = begin_slot();
+            if (!ok) return;
+            const uint32_t dst = smem_u32(sSlots) + s * C::SLOT_BYTES + (c >> 3) * C::CH_BYTES;
+            const __nv_bfloat16* src0 = cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + c * 8;
+#pragma unroll
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int rr = i * RPI + lane / LPR;
+                const int row = __shfl_sync(0xffffffffu, rows, rr);
+                const int r = pw * 32 + rr;
+                cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           src0 + max(row, 0) * rstride, row >= 0 ? 16 : 0);
+            }
+            end_slot();
+        };
+        auto load_q = [&](const ExUnit& U, uint32_t unit) {
+            const uint32_t b = unit % C::QB;
+            if (unit >= static_cast<uint32_t>(C::QB)) await(&q_empty[b], ((unit / C::QB) - 1) & 1);
+            if (!ok) return;
+            const uint32_t dst = smem_u32(sQ) + b * C::Q_BYTES;
+            constexpr int CPR = D / 8;  // 16-byte pieces per row
+            for (int e = pt; e < R * CPR; e += EX_PROD_WARPS * 32) {
+                const int r = e / CPR, c = e % CPR;
+                const bool in = (r >> 1) < U.tvalid;
+                const int t = in ? r >> 1 : 0;
+                const __nv_bfloat16* src = P.q +
+                    (static_cast<size_t>(U.qrow + t) * P.H + 2 * U.g + (r & 1)) * D + c * 8;
+                cp_async16(dst + (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src,
+                           in ? 16 : 0);
+            }
+        };
+        // K of tile x+1 goes before V of tile x, the order of their use
+        ExUnit U;
+        int rows_v = -1, g_v = 0;
+        uint32_t unit = 0;
+        int t = 0;
+        for (long long x = x0; x <= x1 && x0 < x1 && ok; ++x) {
+            int rows = -1;
+            if (x < x1) {
+                const bool next = x == x0 || t + 1 >= U.tiles;
+                if (next) {
+                    ex_unit<C::TQ>(P, cum, x, U);
+                    t = static_cast<int>(x - U.first);
+                    load_q(U, unit++);
+                    if (!ok) break;
+                } else {
+                    ++t;
+                }
+                rows = row_of(U, t);
+                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.k, U.g, rows, s);
+            }
+            if (x > x0)
+                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.v, g_v, rows_v, s);
+            rows_v = rows;
+            g_v = U.g;
+        }
+        cp_async_wait<0>();
+        tell_to(fill);
+    } else if (warp == EX_WARP_MMA) {
+        // ------------------------------------------------------ UMMA issuer
+        if (lane == 0 && x0 < x1) {
+            constexpr uint32_t IDESC_S = idesc_bf16(128, R, false);
+            constexpr uint32_t IDESC_O = idesc_bf16(128, R, false) | (1u << 15);  // A MN-major
+            constexpr uint32_t HI = sdesc_hi(1024);
+            const uint32_t k_lo0 = sdesc_lo(smem_u32(sSlots), 16);
+            const uint32_t v_lo0 = sdesc_lo(smem_u32(sSlots), C::CH_BYTES);  // 64-column chunks
+            const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
+            const uint32_t p_lo0 = sdesc_lo(smem_u32(sP), 16);
+            const uint32_t tmem_o = tmem + 2 * R;
+            uint32_t fill = 0, unit = 0;
+            bool ok = true;
+            // Unit of the S product and tiles of it still to come; the PV
+            // product runs one tile behind and only needs to know the first
+            // and last tile of a unit.
+            ExUnit U;
+            int left = 0;
+            bool first_v = true, last_v = false;  // of the tile that waits for PV
+            for (long long x = x0; x <= x1 && ok; ++x) {
+                const uint32_t it = static_cast<uint32_t>(x - x0);
+                bool first_s = false, last_s = false;
+                if (x < x1) {
+                    if (left == 0) {
+                        ex_unit<C::TQ>(P, cum, x, U);
+                        const long long end = U.first + U.tiles;
+                        left = static_cast<int>((end < x1 ? end : x1) - x);
+                        first_s = true;
+                        ++unit;
+                    }
+                    last_s = --left == 0;
+                    const uint32_t qb = (unit - 1) % C::QB;
+                    const uint32_t q_lo = q_lo0 + qb * (C::Q_BYTES >> 4);
+                    for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
+                        const uint32_t slot = fill % C::NS;
+                        ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
+                                       SITE_EX_MMA);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a0 = k_lo0 + slot * (C::SLOT_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < C::SLOT_COLS / 16; ++kk)
+                            umma_ss_lh(tmem + (it & 1) * R,
+                                       a0 + (kk / 4) * (C::CH_BYTES >> 4) + (kk % 4) * 2,
+                                       q_lo + (s * C::NCH + kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
+                                       HI, IDESC_S, (s | kk) != 0);
+                        umma_commit(&slot_empty[slot]);
+                    }
+                    if (!ok) break;
+                    umma_commit(&s_full[it & 1]);
+                    if (last_s) umma_commit(&q_empty[qb]);
+                }
+                if (x > x0) {
+                    const uint32_t pv = it - 1, b = pv & 1;
+                    ok = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t p_lo = p_lo0 + b * (C::P_BYTES >> 4);
+                    for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
+                        const uint32_t slot = fill % C::NS;
+                        ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
+                                       SITE_EX_MMA);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a0 = v_lo0 + slot * (C::SLOT_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < EX_BN / 16; ++kk)
+                            umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4),
+                                       p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2, HI,
+                                       IDESC_O, !(first_v && kk == 0));
+                        umma_commit(&slot_empty[slot]);
+                    }
+                    if (!ok) break;
+                    umma_commit(&p_empty[b]);
+                    if (last_v) umma_commit(o_full);
+                }
+                first_v = first_s;
+                last_v = last_s;
+            }
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, lim);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        const int wg = warp >> 2, qd = warp & 3;
+        const int key_l = (qd << 5) | lane;                  // key of the tile == TMEM lane
+        const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
+        const uint32_t s_addr = tmem + lane_addr + wg * HC;
+        const uint32_t o_addr = tmem + lane_addr + 2 * R + wg * HC;
+        // P: row r, this thread's pair of keys (even, odd): one 32-bit word
+        const uint32_t p_word = smem_u32(sP) + (key_l >> 6) * (R * 128) + (key_l & 62) * 2;
+        const bool odd = lane & 1;
+        bool ok = true;
+        uint32_t unit = 0;
+        long long x = x0;
+        while (x < x1 && ok) {
+            ExUnit U;
+            ex_unit<C::TQ>(P, cum, x, U);
+            const long long end = U.first + U.tiles;
+            const int t_begin = static_cast<int>(x - U.first);
+            const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
+            float l32[HC], lr[HC], m[HC];
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                l32[c] = lr[c] = 0.f;
+                m[c] = -INFINITY;
+            }
+            for (int t = t_begin; t < t_end; ++t) {
+                const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
+                const uint32_t b = it & 1;
+                ok = mbar_wait(&s_full[b], (it >> 1) & 1, abort_flag, lim, SITE_EX_SM);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                float p[HC];
+                ex_tmem_ld<HC>(s_addr + b * R, p);
+                const int key = U.lo + t * EX_BN + key_l;
+                // every row sees every key of an inner tile
+                const int k0 = U.lo + t * EX_BN;
+                const bool edge = k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
+                                  (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window);
+                if (FIX || P.has_cap) {
+                    // cap in log2 units, minus the fixed shift
+                    const float sh = FIX ? P.cap_l2 - P.fixed_ref : P.cap_l2;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        p[c] = fmaf(-2.0f * P.cap_l2, rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)), sh);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) p[c] *= P.scale_l2;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        const int pos = U.p0 + ((wg * HC + c) >> 1);
+                        if (key > pos || key >= U.hi || (P.window > 0 && pos - key >= P.window))
+                            p[c] = -INFINITY;
+                    }
+                }
+                if constexpr (!FIX) {
+                    float mx[HC];
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) mx[c] = p[c];
+                    const float w = ex_reduce<HC, true>(mx);
+                    float* st = s_max + ((it & 1) * 2 + wg) * 4 * HC;
+                    if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
+                    mbar_arrive(&wg_max[wg]);
+                    ok = mbar_wait(&wg_max[wg], it & 1, abort_flag, lim, SITE_EX_SM);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    bool grow = false, any = false;
+                    float nm[HC];
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) {
+                        nm[c] = fmaxf(fmaxf(st[c], st[HC + c]), fmaxf(st[2 * HC + c], st[3 * HC + c]));
+                        // a row's first finite max needs no rescaling, its O is zero
+                        any |= nm[c] > m[c];
+                        grow |= nm[c] > m[c] + EX_RESCALE_LOG2 && m[c] != -INFINITY;
+                    }
+                    // (the same decision in all threads of the warpgroup)
+                    if (grow && t > t_begin) {
+                        const uint32_t pv = it - 1;  // O must hold every tile before this
+                        ok = mbar_wait(&p_empty[pv & 1], (pv >> 1) & 1, abort_flag, lim, SITE_EX_SM);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) {
+                            const float n = fmaxf(m[c], nm[c]);
+                            const float f = m[c] == -INFINITY ? 1.0f : ex2_approx(m[c] - n);
+                            m[c] = n;
+                            l32[c] *= f;
+                            lr[c] *= f;
+                            nm[c] = f;
+                        }
+#pragma unroll
+                        for (int o = 0; o < C::O_BLOCKS; ++o) {
+                            float a[HC];
+                            ex_tmem_ld<HC>(o_addr + o * R, a);
+#pragma unroll
+                            for (int c = 0; c < HC; ++c) a[c] *= nm[c];
+                            ex_tmem_st<HC>(o_addr + o * R, a);
+                        }
+                        tmem_wait_st();
+                    } else if (any) {
+#pragma unroll
+                        for (int c = 0; c < HC; ++c)
+                            if (m[c] == -INFINITY) m[c] = nm[c];
+                    }
+#pragma unroll
+                    for (int c = 0; c < HC; ++c) p[c] -= m[c] == -INFINITY ? 0.f : m[c];
+                }
+                if (it >= 2) {  // P buffer: the product of tile it - 2 has read it
+                    ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    p[c] = ex2_approx(p[c]);
+                    l32[c] += p[c];
+                }
+                // rows c and c + 4: lanes 2j, 2j+1 swap halves and store the key
+                // pair of one row each (a warp's store hits every bank once)
+#pragma unroll
+                for (int c8 = 0; c8 < HC; c8 += 8) {
+#pragma unroll
+                    for (int c = c8; c < c8 + 4; ++c) {
+                        const uint32_t own = pack_bf16x2(p[c], p[c + 4]);
+                        lr[c] += __uint_as_float(own << 16);
+                        lr[c + 4] += __uint_as_float(own & 0xFFFF0000u);
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
+                        const uint32_t w = odd ? __byte_perm(got, own, 0x7632)
+                                               : __byte_perm(own, got, 0x5410);
+                        const int r = wg * HC + c + (odd ? 4 : 0);
+                        const uint32_t a = (p_word + b * C::P_BYTES + r * 128) ^ ((r & 7) << 4);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w) : "memory");
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(&p_full[b]);
+            }
+            if (!ok) break;
+            // row sums over the 128 keys' threads
+            float* ssum = s_sum + ((unit & 1) * 2 + wg) * 4 * HC * 2;
+            {
+                const float a = ex_reduce<HC, false>(l32);
+                const float r = ex_reduce<HC, false>(lr);
+                if ((lane & (32 / HC - 1)) == 0) {
+                    ssum[(qd * HC + ex_col<HC>(lane)) * 2] = a;
+                    ssum[(qd * HC + ex_col<HC>(lane)) * 2 + 1] = r;
+                }
+                mbar_arrive(&wg_sum[wg]);
+                ok = mbar_wait(&wg_sum[wg], unit & 1, abort_flag, lim, SITE_EX_SM);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            ok = mbar_wait(o_full, unit & 1, abort_flag, lim, SITE_EX_SM);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const bool whole = t_begin == 0 && t_end == U.tiles;
+            // a stretch's first segment has slot 0, its last one slot 1
+            const size_t ws = static_cast<size_t>(blockIdx.x) * 2 + (unit == 0 ? 0 : 1);
+            const int rows = 2 * U.tvalid;
+#pragma unroll
+            for (int o = 0; o < C::O_BLOCKS; ++o) {
+                float a[HC];
+                ex_tmem_ld<HC>(o_addr + o * R, a);
+                const int dcol = o * 128 + key_l;
+                if (D < 128 && key_l >= D) continue;
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    const int r = wg * HC + c;
+                    if (r >= rows) continue;
+                    if (whole) {
+                        float l = 0.f;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) l += ssum[(w * HC + c) * 2 + 1];
+                        const float v = l > 0.f ? a[c] / l : 0.f;
+                        P.out[(static_cast<size_t>(U.qrow + (r >> 1)) * P.H + 2 * U.g + (r & 1)) * D +
+                              dcol] = __float2bfloat16_rn(v);
+                    } else {
+                        P.ws_o[(ws * R + r) * D + dcol] = a[c];
+                    }
+                }
+            }
+            if (key_l < HC && wg * HC + key_l < rows) {
+                const int r = wg * HC + key_l;
+                float a = 0.f, l = 0.f, mm = FIX ? P.fixed_ref : -INFINITY;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    a += ssum[(w * HC + key_l) * 2];
+                    l += ssum[(w * HC + key_l) * 2 + 1];
+                }
+                if constexpr (!FIX) {
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        if (c == key_l) mm = m[c];
+                }
+                if (!whole) {
+                    float* s = P.ws_s + (ws * R + r) * 4;
+                    s[0] = mm;
+                    s[1] = a;
+                    s[2] = l;
+                } else if (P.lse != nullptr) {
+                    P.lse[static_cast<size_t>(2 * U.g + (r & 1)) * P.total_q + U.qrow + (r >> 1)] =
+                        a > 0.f ? (mm + log2f(a)) * 0.69314718055994531f : -INFINITY;
+                }
+            }
+            tc_fence_before();
+            x += t_end - t_begin;
+            ++unit;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == EX_WARP_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Joins the partial results of units that more than one CTA worked on. CTA c
+// looks at the start of stretch c + 1: where that cuts a unit, the unit's n
+// cuts share its rows and columns between them.
+//   M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
+template <int D, int R>
+__global__ void __launch_bounds__(256) extend_merge(const ExParams P, int grid) {
+    using C = ExCfg<D, R>;
+    __shared__ long long cum[EX_MAX_SEQS + 1];
+    ex_cum<C::TQ>(P, cum);
+    const long long all = cum[P.num_seqs];
+    const long long ctas = ex_ctas(P, all, grid);
+    const long long cut = blockIdx.x + 1ll;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (cut >= ctas) return;
+    const long long x = ex_start(cut, all, ctas);
+    ExUnit U;
+    ex_unit<C::TQ>(P, cum, x, U);
+    if (U.first == x) return;
+    const int c0 = static_cast<int>(ex_owner(U.first, all, ctas));
+    const int c1 = static_cast<int>(ex_owner(U.first + U.tiles - 1, all, ctas));
+    const int share = static_cast<int>(cut) - c0 - 1, shares = c1 - c0;
+    // the unit is its first CTA's last segment (slot 1 unless it is also its
+    // first) and every other CTA's first
+    const bool c0_first = ex_start(c0, all, ctas) >= U.first;
+    const int n = 2 * U.tvalid * (D / 4);
+    for (int e = share * 256 + threadIdx.x; e < n; e += shares * 256) {
+        const int r = e / (D / 4), c = e % (D / 4);
+        float M = -INFINITY;
+        for (int i = c0; i <= c1; ++i) {
+            const size_t ws = static_cast<size_t>(i) * 2 + (i == c0 && !c0_first ? 1 : 0);
+            M = fmaxf(M, P.ws_s[(ws * R + r) * 4]);
+        }
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float a = 0.f, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = c0; i <= c1; ++i) {
+            const size_t ws = static_cast<size_t>(i) * 2 + (i == c0 && !c0_first ? 1 : 0);
+            const float4 st = *reinterpret_cast<const float4*>(P.ws_s + (ws * R + r) * 4);
+            const float4 v = *reinterpret_cast<const float4*>(P.ws_o + (ws * R + r) * D + 4 * c);
+            const float w = ex2_approx(st.x - Mu);
+            a = fmaf(w, st.y, a);
+            l = fmaf(w, st.z, l);
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        const int qrow = U.qrow + (r >> 1), h = 2 * U.g + (r & 1);
+        *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(qrow) * P.H + h) * D + 4 * c) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c == 0 && P.lse != nullptr)
+            P.lse[static_cast<size_t>(h) * P.total_q + qrow] =
+                a > 0.f ? (M + log2f(a)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+}  // namespace g2

@@ -1,6 +1,7 @@
 /*
  * g2attn.h -- libg2attn: Gemma 2 soft-capped local/global attention (forward,
- * decode and gradients) for NVIDIA B200 (sm_100a).
+ * decode and gradients) and what goes round it in a model with a KV cache
+ * (rotary positions, cache appends, pages) for NVIDIA B200 (sm_100a).
  *
  * The operation (Gemma 2 card, "Method", per-layer attention pseudo-code; the
  * soft-cap formula is the "Gemma 2 Guide", section 1): for every query row i
@@ -60,8 +61,10 @@ typedef enum {
     G2ATTN_ERR_CUDA = 4,           /* a CUDA runtime/driver call or launch failed */
     G2ATTN_ERR_DEVICE_TIMEOUT = 5, /* a kernel gave up waiting (see g2attn_get_device_error) */
     G2ATTN_ERR_WORKSPACE = 6,      /* a workspace NULL or smaller than required */
-    G2ATTN_ERR_CACHE_LEN = 7       /* a decode sequence saw more keys than max_cache_len
+    G2ATTN_ERR_CACHE_LEN = 7,      /* a decode sequence saw more keys than max_cache_len
                                       planned for (see g2attn_get_device_error) */
+    G2ATTN_ERR_CACHE_ROW = 8       /* an appended token had no row in its cache and was
+                                      dropped (see g2attn_get_device_error) */
 } g2attn_status;
 
 /*
@@ -306,6 +309,208 @@ G2ATTN_API int g2attn_prefill_varlen_backward(const void* q, const void* k, cons
                                    float query_scale, float softcap, int window, void* workspace,
                                    size_t workspace_bytes, g2attn_stream_t stream);
 
+/*
+ * Rotary positions of the queries and keys of num_tokens tokens (before any of
+ * the attention calls), and their gradients. For a token at position p and
+ * pair i < rotary_dim / 2, with a = 2 pi p w_i and m = mscale,
+ *   y1 = m (x1 cos a - x2 sin a),   y2 = m (x2 cos a + x1 sin a);
+ * elements rotary_dim .. d-1 of a head are copied.
+ *   q (num_tokens, H, d) with q_stride elements from token to token, k
+ *   (num_tokens, Hkv, d) with k_stride (so that both may be cut out of one
+ *   projection); q_out and k_out alike with their own strides. In place
+ *   (q_out == q with equal strides; the same for k) is allowed, other overlaps are not.
+ *   positions: device int32 [num_tokens], any values.
+ *   freqs: device uint64 [rotary_dim / 2], the fraction of a turn per position
+ *   times 2^64, w_i mod 1 in fixed point: phases of any int32 position are
+ *   then right to 2^-32 turns, where a float product would lose them.
+ *   rotary_dim: a multiple of 16, 16 .. d (other multiples: UNSUPPORTED).
+ *   interleaved: 0 pairs elements (i, i + rotary_dim / 2), nonzero (2i, 2i + 1).
+ *   mscale: factor on the rotation (long-context scalings use one), 1 for none.
+ *   inverse: 0 the rotation; nonzero its transpose, which turns the gradients
+ *   of q_out and k_out (given as q and k) into those of q and k.
+ * d = 64, 128 or 256; any H and Hkv >= 1; strides multiples of 8 elements, at
+ * least one token's elements. fp32 arithmetic, one rounding to bf16.
+ */
+G2ATTN_API int g2attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                const int* positions, const unsigned long long* freqs, int num_tokens, int H,
+                int Hkv, int d, int rotary_dim, int interleaved, float mscale, int inverse,
+                long long q_stride, long long k_stride, long long q_out_stride,
+                long long k_out_stride, g2attn_stream_t stream);
+
+/*
+ * Rotary positions and cache append in one pass: the T_s new tokens of
+ * sequence s sit at its last positions (L_s - T_s .. L_s - 1, L_s its length
+ * with them); their queries are rotated into q_out, their keys rotated into
+ * the cache and their values copied there, into the rows that the attention
+ * calls read. This call: a packed cache (g2attn_decode, g2attn_prefill_varlen).
+ *   q, k, v as g2attn_rope's q and k (v with v_stride); q_out (total_q, H, d)
+ *   packed, in place allowed where q is packed too; freqs, rotary_dim,
+ *   interleaved, mscale as g2attn_rope.
+ *   k_cache, v_cache (total_k, Hkv, d) packed by cu_seqlens_k (device int32,
+ *   num_seqs + 1 entries), whose differences are the L_s.
+ *   cu_seqlens_q: device int32, num_seqs + 1 non-decreasing entries from 0 (T_s
+ *   may be 0), or NULL when every sequence has exactly one new token (then
+ *   total_q must equal num_seqs). Rows of q_out at and behind
+ *   cu_seqlens_q[num_seqs] are left as they are.
+ *   A token that has no row in its cache (T_s > L_s, lengths past the cache)
+ *   writes nothing to it, and g2attn_get_device_error reports
+ *   G2ATTN_ERR_CACHE_ROW. Nothing outside the tensors is touched.
+ */
+G2ATTN_API int g2attn_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                       void* k_cache, void* v_cache, const int* cu_seqlens_q,
+                       const int* cu_seqlens_k, const unsigned long long* freqs, int num_seqs,
+                       int total_q, int total_k, int H, int Hkv, int d, int rotary_dim,
+                       int interleaved, float mscale, long long q_stride, long long k_stride,
+                       long long v_stride, g2attn_stream_t stream);
+
+/*
+ * The same into ring caches (num_seqs, ring_size, Hkv, d) as g2attn_decode_ring
+ * reads them: position p in slot p mod ring_size (a power of two); seq_lens:
+ * device int32 [num_seqs], the L_s. Of a chunk longer than the ring only the
+ * last ring_size tokens are stored (the others would be overwritten by them).
+ */
+G2ATTN_API int g2attn_rope_append_ring(const void* q, const void* k, const void* v, void* q_out,
+                            void* k_ring, void* v_ring, const int* cu_seqlens_q,
+                            const int* seq_lens, const unsigned long long* freqs, int num_seqs,
+                            int total_q, int ring_size, int H, int Hkv, int d, int rotary_dim,
+                            int interleaved, float mscale, long long q_stride,
+                            long long k_stride, long long v_stride, g2attn_stream_t stream);
+
+/*
+ * The same into paged caches (num_blocks, block_size, Hkv, d) as
+ * g2attn_decode_paged, g2attn_extend_paged and g2attn_prefill_paged read them;
+ * seq_lens: device int32 [num_seqs], the L_s; block_size a power of two. A token
+ * whose table entry lies outside [0, num_blocks) has no row (see above). Pages
+ * that several sequences share are not copied: the caller's tables name
+ * pages of their own for the rows written here (g2attn_pages_fork leaves them so).
+ */
+G2ATTN_API int g2attn_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                             void* k_blocks, void* v_blocks, const int* cu_seqlens_q,
+                             const int* block_table, const int* seq_lens,
+                             const unsigned long long* freqs, int num_seqs, int total_q,
+                             int num_blocks, int block_size, int max_blocks_per_seq, int H,
+                             int Hkv, int d, int rotary_dim, int interleaved, float mscale,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             g2attn_stream_t stream);
+
+/*
+ * Bytes of device workspace g2attn_extend_paged needs: partial results of the
+ * units that more than one CTA works on. Depends only on the arguments; 0 for
+ * arguments that call would refuse.
+ */
+G2ATTN_API size_t g2attn_extend_workspace_size(int max_T, int d);
+
+/*
+ * Attention of a short chunk of new tokens per sequence over a paged KV cache
+ * (checking proposed tokens, the tail of a prompt, one token): the operation
+ * of g2attn_prefill_paged, for pages of any power of two of rows and with the
+ * keys of long caches split over all SMs. Chunks of at most some tens of tokens
+ * are what it is made for; longer ones are taken in units of 32 positions
+ * that each read the keys again.
+ *   q (total_q, H, d) packed by cu_seqlens_q (device int32, num_seqs + 1
+ *   non-decreasing entries from 0; T_s may be 0); out like q; lse (H, total_q)
+ *   fp32 or NULL. Rows behind cu_seqlens_q[num_seqs] are left as they are.
+ *   k_blocks, v_blocks, block_table, seq_lens (L_s, the new tokens included:
+ *   append them first) as g2attn_decode_paged. Rows of pages beyond L_s are
+ *   not read. Table entries outside [0, num_blocks) are clamped; malformed
+ *   lengths or tables give undefined results, never an out-of-bounds access.
+ *   A query that sees no key (T_s > L_s) gets out = 0 and lse = -inf.
+ *   max_T: the longest chunk the caller expects; it picks the kernel's row count
+ *   (16, 32 or 64 rows for chunks of up to 8, 16 or more positions) and the
+ *   workspace. Longer chunks than max_T are still right.
+ *   workspace: at least g2attn_extend_workspace_size(max_T, d) bytes, 16-byte
+ *   aligned, no initial contents needed. Calls that may run at the same time
+ *   (two streams, two graphs) need workspaces of their own.
+ * Limits: num_seqs <= 1024 (as g2attn_prefill_varlen). Two kernels on `stream`.
+ */
+G2ATTN_API int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_blocks,
+                        void* out, float* lse, const int* cu_seqlens_q, const int* block_table,
+                        const int* seq_lens, int num_seqs, int total_q, int num_blocks,
+                        int block_size, int max_blocks_per_seq, int max_T, int H, int Hkv, int d,
+                        float query_scale, float softcap, int window, void* workspace,
+                        size_t workspace_bytes, g2attn_stream_t stream);
+
+/*
+ * Pages of a paged cache. Common to the calls below:
+ *   block_table: device int32 [num_seqs][max_blocks_per_seq]; entries behind a
+ *   sequence's last page are -1. seq_lens: device int32 [num_seqs] (0: an empty
+ *   slot). ref_counts: device int32 [num_blocks], 16-byte aligned: how many
+ *   table entries name each page, 0 for a free one. All three are the caller's;
+ *   start with -1, 0 and 0. block_size: a power of two.
+ *   Fresh pages are the free ones of lowest index, given to the sequences in
+ *   their order; a request is granted when the pages asked for by it and by
+ *   all sequences before it (granted or not) are free. granted: device int32
+ *   [num_seqs], 1 or 0; what is refused is left unchanged.
+ *   workspace: g2attn_pages_workspace_size bytes of device memory, 16-byte
+ *   aligned, no initial contents needed, not shared by calls that may overlap.
+ * Nothing outside the arrays is touched, whatever they hold. Calls on one set
+ * of tables are ordered by the caller (one stream).
+ */
+G2ATTN_API size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks);
+
+/*
+ * Makes every sequence s longer by add[s] rows (device int32; 0 or less: as it
+ * is): fresh pages for the rows past its last page, seq_lens[s] += add[s].
+ * Refused when the pages run out or the table row is too short.
+ */
+G2ATTN_API int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
+                      int* granted, int num_seqs, int num_blocks, int block_size,
+                      int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
+                      g2attn_stream_t stream);
+
+/*
+ * Cuts every sequence s to min(its length, max(keep[s], 0)) rows (device int32)
+ * and gives the pages behind them back (their counts drop by one; 0: free).
+ * keep[s] = 0 frees the sequence; keep[s] >= its length leaves it.
+ */
+G2ATTN_API int g2attn_pages_truncate(int* block_table, int* seq_lens, int* ref_counts,
+                          const int* keep, int num_seqs, int num_blocks, int block_size,
+                          int max_blocks_per_seq, g2attn_stream_t stream);
+
+/*
+ * Every sequence s becomes a fork of sequence parents[s] (device int32; s itself
+ * or a value outside [0, num_seqs): stays), all at once, as beam search
+ * reorders its beams: a parent may be taken several times and be replaced
+ * itself. Full pages are shared (counts), a partly filled last page is replaced
+ * by a fresh one whose contents the caller copies with g2attn_pages_copy from
+ * copy_src[s] to copy_dst[s] (device int32 [num_seqs], -1: nothing to copy); the
+ * pages that s had are given back, but only after fresh ones were picked, so
+ * no copy reads a page that another one writes.
+ * new_table and new_lens (other arrays than block_table and seq_lens, which
+ * stay as they are) get the result; a refused sequence keeps its pages.
+ */
+G2ATTN_API int g2attn_pages_fork(const int* block_table, const int* seq_lens, const int* parents,
+                      int* new_table, int* new_lens, int* ref_counts, int* copy_src,
+                      int* copy_dst, int* granted, int num_seqs, int num_blocks, int block_size,
+                      int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
+                      g2attn_stream_t stream);
+
+/*
+ * Moves the live pages (count > 0) to the front of the cache: with n live
+ * pages, the i-th live page at or above index n goes to the i-th free page below
+ * it. Updates the table and the counts; copy_src and copy_dst (device int32
+ * [num_blocks / 2], padded with -1) list the moves for g2attn_pages_copy, and
+ * num_live (device int32) gets n. All caches indexed by the table must then
+ * be copied before they are read.
+ */
+G2ATTN_API int g2attn_pages_compact(int* block_table, int* ref_counts, int* copy_src,
+                         int* copy_dst, int* num_live, int num_seqs, int num_blocks,
+                         int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
+                         g2attn_stream_t stream);
+
+/*
+ * Copies page src[i] to page dst[i] (device int32 [num_pairs]) in each of
+ * num_caches caches (K and V of every layer; `caches` is a host array of device
+ * pointers, 16-byte aligned, each num_blocks * page_bytes long). Pairs with an
+ * index outside [0, num_blocks) are skipped. A page that is written must not be
+ * read or written by another pair (the pairs of fork and compact are so).
+ * page_bytes: a multiple of 16, else UNSUPPORTED. The array is read before the
+ * call returns. One kernel per 128 caches.
+ */
+G2ATTN_API int g2attn_pages_copy(void* const* caches, int num_caches, const int* src,
+                      const int* dst, int num_pairs, int num_blocks, size_t page_bytes,
+                      g2attn_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 G2ATTN_API const char* g2attn_status_string(int status);
 
@@ -315,10 +520,12 @@ G2ATTN_API const char* g2attn_status_string(int status);
  * met a sequence whose visible keys need more splits than its max_cache_len
  * planned for: that call still returned G2ATTN_OK and stayed inside its
  * buffers, but dropped the keys past the plan, so its output for that
- * sequence is wrong. Reading the word synchronizes the device and clears it.
- * Returns G2ATTN_OK when clear, G2ATTN_ERR_DEVICE_TIMEOUT when a wait gave up
- * (this takes precedence), G2ATTN_ERR_CACHE_LEN when only the decode
- * precondition was broken, G2ATTN_ERR_CUDA if the word cannot be read.
+ * sequence is wrong. It is also set when an append call dropped a token that
+ * had no row in its cache. Reading the word synchronizes the device and clears
+ * it. Returns G2ATTN_OK when clear, G2ATTN_ERR_DEVICE_TIMEOUT when a wait gave up
+ * (this takes precedence), then G2ATTN_ERR_CACHE_LEN for the decode
+ * precondition, G2ATTN_ERR_CACHE_ROW when only tokens were dropped,
+ * G2ATTN_ERR_CUDA if the word cannot be read.
  */
 G2ATTN_API int g2attn_get_device_error(void);
 
