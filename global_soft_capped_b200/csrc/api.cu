@@ -629,7 +629,8 @@ int append_common(g2::RopeParams& P, const void* v, void* v_cache, const int* cu
 int extend_rows(int max_T) { return max_T <= 8 ? 16 : (max_T <= 16 ? 32 : 64); }
 
 size_t extend_ws_bytes(int max_T, int d) {
-    return 2ull * g2::EX_MAX_CTAS * extend_rows(max_T) * (static_cast<size_t>(d) + 4) * sizeof(float);
+    return 2ull * g2::EX_MAX_CTAS *
+           (sizeof(int4) + extend_rows(max_T) * (static_cast<size_t>(d) + 4) * sizeof(float));
 }
 
 template <int D, int R, int SM>
@@ -655,7 +656,7 @@ int launch_extend(g2::ExParams& P, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, g2::extend_merge<D, R>, static_cast<const g2::ExParams>(P), grid) !=
+    if (cudaLaunchKernelEx(&cfg, g2::extend_merge<D, R>, static_cast<const g2::ExParams>(P)) !=
         cudaSuccess)
         return G2ATTN_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
@@ -1194,7 +1195,8 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     P.cu_q = cu_seqlens_q;
     P.table = block_table;
     P.lens = seq_lens;
-    P.ws_s = static_cast<float*>(workspace);
+    P.ws_rec = static_cast<int4*>(workspace);
+    P.ws_s = reinterpret_cast<float*>(P.ws_rec + 2 * g2::EX_MAX_CTAS);
     P.ws_o = P.ws_s + 2ull * g2::EX_MAX_CTAS * extend_rows(max_T) * 4;
     P.num_seqs = num_seqs;
     P.total_q = total_q;
@@ -1208,6 +1210,14 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     fill_cap(query_scale, softcap, P.k_exp, P.cap_l2, P.scale_l2, P.has_cap);
     const bool fixed = P.has_cap && P.cap_l2 <= g2::PF_FIXED_REF_MAX;
     P.fixed_ref = fixed ? P.cap_l2 - 64.0f : 0.f;
+    g2::PfParams F{};  // the forward's bound on where the series serves
+    fill_poly(query_scale, softcap, F);
+    const float us2 = F.u_scale * F.u_scale;
+    P.series[0] = P.scale_l2;
+    P.series[1] = P.scale_l2 * g2::kTanhC1 * us2;
+    P.series[2] = P.scale_l2 * g2::kTanhC2 * us2 * us2;
+    P.series[3] = P.scale_l2 * g2::kTanhC3 * us2 * us2 * us2;
+    P.series_max = P.has_cap && isfinite(F.poly_acc_max) ? F.poly_acc_max : 0.f;
     P.timeout_ns = wait_limit_ns();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     switch (d) {

@@ -24,20 +24,24 @@
 // sums) in the workspace, at most two per CTA, and extend_merge joins them in
 // the order of the keys (no atomics: results do not depend on timing).
 //
-// One CTA of 416 threads per SM:
+// One CTA of 384 threads per SM:
 //   warps 0..7   softmax: warpgroup w/4 takes rows w/4*R/2 .. of S^T, thread =
 //                key; writes P as bf16 into shared memory; at a unit's end
 //                reads O^T (lane = d column) and writes out or the partial.
 //   warp 8       tensor memory, one thread issues the UMMAs.
-//   warps 9..12  producers: 16-byte asynchronous copies of Q, K and V rows into
+//   warps 9, 10  producers: 16-byte asynchronous copies of Q, K and V rows into
 //                128-byte-swizzled tiles. Each row's page is looked up, so
 //                pages may be of any size; rows behind the last visible key
 //                are filled with zeros (what the cache holds there, NaN
 //                included, does not matter).
-// Softmax: fp32, log2 domain, the fixed shift of the prefill when the cap
-// allows it, else a running max with lazy rescaling of O (when a max grows by
-// more than 2^8). P is rounded to bf16 for the product; out is
-// normalised by the sum of the rounded weights, lse uses the unrounded sum.
+//   warp 11      writes the CTA's merge record.
+// Softmax: fp32, log2 domain. With the cap the prefill's fixed shift where it
+// fits. Else a reference per row that is the row's maximum over its first tile
+// and is only raised (and O and the sums rescaled) when a score passes it by
+// more than 2^64: weights up to 2^64 lose nothing in fp32 or bf16, and the usual tile
+// needs one vote per warp and no exchange of maxima. P is rounded to bf16 for
+// the product; out is normalised by the sum of the rounded weights, lse
+// uses the unrounded sum.
 #pragma once
 
 #include "common.cuh"
@@ -49,11 +53,13 @@ constexpr int EX_BN = 128;            // keys per tile
 constexpr int EX_SM_THREADS = 256;    // softmax warps 0..7
 constexpr int EX_WARP_MMA = 8;
 constexpr int EX_WARP_PROD = 9;
-constexpr int EX_PROD_WARPS = 4;
-constexpr int EX_THREADS = 416;
+constexpr int EX_PROD_WARPS = 2;
+constexpr int EX_WARP_RECORD = 11;
+constexpr int EX_THREADS = 384;       // 12 warps: up to 168 registers per thread
 constexpr int EX_MAX_SEQS = 1024;     // per-launch table in shared memory
 constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
-constexpr float EX_RESCALE_LOG2 = 8.0f;
+constexpr float EX_RAISE_LOG2 = 64.0f;   // see the softmax above
+constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key yet
 
 template <int D, int R>
 struct ExCfg {
@@ -72,7 +78,7 @@ struct ExCfg {
     // tiles after the ring must span that
     static constexpr int PAD = D == 64 && FIXED < CH_BYTES ? CH_BYTES - FIXED : 0;
     static constexpr int CUM_BYTES = 8 * (EX_MAX_SEQS + 1);
-    static constexpr int CTRL_BYTES = 256 + 2 * 2 * 4 * HC * 12;
+    static constexpr int CTRL_BYTES = 320 + 2 * 2 * 4 * HC * 12 + 2 * 2 * HC * 4;
     static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - PAD - CUM_BYTES - CTRL_BYTES - 64;
     static constexpr int NS_FIT = BUDGET / SLOT_BYTES;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
@@ -94,10 +100,13 @@ struct ExParams {
     const int* table;
     const int* lens;
     float* ws_o;     // [2 * EX_MAX_CTAS][R][D]
-    float* ws_s;     // [2 * EX_MAX_CTAS][R][4]: max, fp32 sum, sum of rounded weights, unused
+    float* ws_s;     // [2 * EX_MAX_CTAS][R][4]: reference, fp32 sum, sum of rounded weights, -
+    int4* ws_rec;    // [EX_MAX_CTAS][2]: merge records
     int num_seqs, total_q, num_blocks, block_shift, max_blocks;
     int H, Hkv, window;
     float k_exp, cap_l2, scale_l2, fixed_ref;
+    float series[4];     // capped score in log2 units = x (s0 + s1 x^2 + s2 x^4 + s3 x^6)
+    float series_max;    // for |x| up to this (|x / C| <= 1/4)
     int has_cap;
     int min_tiles;   // tiles a CTA takes at least
     unsigned long long timeout_ns;
@@ -210,29 +219,18 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+// Arrives on `bar` once every copy this thread issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp_async_wait_all() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
-// Shared-memory writes of this thread before, tensor-core reads after.
+// Shared-memory writes ordered before this thread (its own, or those it waited
+// for at an mbarrier) come before the tensor core's reads issued after this.
 __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Whether the phase of the given parity has completed, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // N = 8, 16 or 32 columns of this warp's 32 TMEM lanes; waits for the data.
@@ -339,12 +337,16 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
     uint64_t* wg_max = bars + 25;          // [2] warpgroup exchanges
     uint64_t* wg_sum = bars + 27;          // [2]
     uint64_t* drain = bars + 29;
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 30);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 31);
-    // row statistics that the warps of a warpgroup exchange: maxima
-    // [tile parity][warpgroup][warp][HC], sums [unit parity][..][..][HC][2]
-    float* s_max = reinterpret_cast<float*>(bars + 32);
+    uint64_t* wg_vote = bars + 30;         // [2]
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 32);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 33);
+    // votes of the warps of a warpgroup, a byte each [tile parity][warpgroup]
+    volatile uint32_t* votes = reinterpret_cast<volatile uint32_t*>(bars + 34);
+    // row statistics that they exchange: maxima [exchange parity][warpgroup]
+    // [warp][HC], sums [unit parity][..][..][HC][2]
+    float* s_max = reinterpret_cast<float*>(bars + 40);
     float* s_sum = s_max + 2 * 2 * 4 * HC;
+    float* s_fac = s_sum + 2 * 2 * 4 * HC * 2;  // [exchange parity][warpgroup][HC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = P.timeout_ns;
@@ -359,6 +361,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             mbar_init(&p_full[i], EX_SM_THREADS);
             mbar_init(&p_empty[i], 1);
             mbar_init(&wg_max[i], 128);
+            mbar_init(&wg_vote[i], 4);
             mbar_init(&wg_sum[i], 128);
         }
         mbar_init(o_full, 1);
@@ -385,63 +388,52 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         x1 = ex_start(blockIdx.x + 1ll, all, ctas);
     }
 
-    if (warp >= EX_WARP_PROD) {
+    if (warp >= EX_WARP_PROD && warp < EX_WARP_RECORD) {
         // -------------------------------------------------------- producers
-        const int pw = warp - EX_WARP_PROD;       // rows pw*32 .. of a tile
+        constexpr int RW = EX_BN / EX_PROD_WARPS;  // rows of a tile per warp
+        constexpr int RL = RW / 32;                // of which a lane looks up this many
+        const int pw = warp - EX_WARP_PROD;
         const int pt = tid - EX_WARP_PROD * 32;
-        uint32_t fill = 0, told = 0;              // slots filled, slots signalled
+        uint32_t fill = 0;                         // slots filled
         bool ok = true;
-        // copies of every filled slot have landed: hand them over
-        auto tell_to = [&](uint32_t upto) {
-            fence_async_smem();
-            for (; told < upto; ++told) mbar_arrive(&slot_full[told % C::NS]);
-        };
         auto await = [&](uint64_t* bar, uint32_t parity) {
-            if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return;
-            cp_async_wait<0>();  // the consumer may need them before it frees this
-            tell_to(fill);
             ok = mbar_wait(bar, parity, abort_flag, lim, SITE_EX_PROD);
             ok = __all_sync(0xffffffffu, ok);
         };
         const long long rstride = static_cast<long long>(P.Hkv) * D;
-        // this lane's row of key tile `base`: its cache row, -1 outside [lo, hi)
-        auto row_of = [&](const ExUnit& U, int tile) -> int {
-            const int key = U.lo + tile * EX_BN + pw * 32 + lane;
-            if (key >= U.hi) return -1;
-            int b = P.table[static_cast<size_t>(U.seq) * P.max_blocks + (key >> P.block_shift)];
-            b = max(0, min(b, P.num_blocks - 1));
-            return (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
-        };
-        auto begin_slot = [&]() -> uint32_t {
-            const uint32_t s = fill % C::NS;
-            if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
-            return s;
-        };
-        auto end_slot = [&]() {
-            cp_async_commit();
-            ++fill;
-            if (fill - told >= static_cast<uint32_t>(C::NS - 1)) {
-                cp_async_wait<C::NS - 2>();
-                tell_to(fill - (C::NS - 2));
+        // this lane's cache rows of key tile `tile`, -1 outside [lo, hi)
+        auto rows_of = [&](const ExUnit& U, int tile, int (&rows)[RL]) {
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                const int key = U.lo + tile * EX_BN + pw * RW + i * 32 + lane;
+                rows[i] = -1;
+                if (key < U.hi) {
+                    int b = P.table[static_cast<size_t>(U.seq) * P.max_blocks +
+                                    (key >> P.block_shift)];
+                    b = max(0, min(b, P.num_blocks - 1));
+                    rows[i] = (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
+                }
             }
         };
         constexpr int LPR = C::SLOT_COLS / 8;  // lanes per row of a slot
         constexpr int RPI = 32 / LPR;          // rows per instruction
-        auto load_tile = [&](const __nv_bfloat16* cache, int g, int rows, int s0) {
+        auto load_tile = [&](const __nv_bfloat16* cache, int g, const int (&rows)[RL], int s0) {
             const int c = lane % LPR;
-            const uint32_t s = begin_slot();
+            const uint32_t s = fill % C::NS;
+            if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
             if (!ok) return;
             const uint32_t dst = smem_u32(sSlots) + s * C::SLOT_BYTES + (c >> 3) * C::CH_BYTES;
             const __nv_bfloat16* src0 = cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + c * 8;
 #pragma unroll
-            for (int i = 0; i < 32 / RPI; ++i) {
+            for (int i = 0; i < RW / RPI; ++i) {
                 const int rr = i * RPI + lane / LPR;
-                const int row = __shfl_sync(0xffffffffu, rows, rr);
-                const int r = pw * 32 + rr;
+                const int row = __shfl_sync(0xffffffffu, rows[i * RPI / 32], rr & 31);
+                const int r = pw * RW + rr;
                 cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                            src0 + max(row, 0) * rstride, row >= 0 ? 16 : 0);
             }
-            end_slot();
+            cp_async_arrive(&slot_full[s]);  // counts the unit's Q rows in, too
+            ++fill;
         };
         auto load_q = [&](const ExUnit& U, uint32_t unit) {
             const uint32_t b = unit % C::QB;
@@ -459,33 +451,56 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                            in ? 16 : 0);
             }
         };
-        // K of tile x+1 goes before V of tile x, the order of their use
+        // K of tile x+1 goes before V of tile x, the order of their use; a
+        // tile's rows are looked up while the one before it loads
         ExUnit U;
-        int rows_v = -1, g_v = 0;
+        int rows[RL], rows_v[RL], ahead[RL], g_v = 0, t = 0;
         uint32_t unit = 0;
-        int t = 0;
         for (long long x = x0; x <= x1 && x0 < x1 && ok; ++x) {
-            int rows = -1;
             if (x < x1) {
-                const bool next = x == x0 || t + 1 >= U.tiles;
-                if (next) {
+                if (x == x0 || t + 1 >= U.tiles) {
                     ex_unit<C::TQ>(P, cum, x, U);
                     t = static_cast<int>(x - U.first);
+                    rows_of(U, t, rows);
                     load_q(U, unit++);
                     if (!ok) break;
                 } else {
                     ++t;
+#pragma unroll
+                    for (int i = 0; i < RL; ++i) rows[i] = ahead[i];
                 }
-                rows = row_of(U, t);
+                if (t + 1 < U.tiles) rows_of(U, t + 1, ahead);
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.k, U.g, rows, s);
             }
             if (x > x0)
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.v, g_v, rows_v, s);
-            rows_v = rows;
+#pragma unroll
+            for (int i = 0; i < RL; ++i) rows_v[i] = rows[i];
             g_v = U.g;
         }
-        cp_async_wait<0>();
-        tell_to(fill);
+        cp_async_wait_all();
+    } else if (warp == EX_WARP_RECORD) {
+        // ----------------------------------------------------- merge record
+        // Where this CTA's stretch starts inside a unit: the unit's rows, the
+        // CTAs c0 .. c1 that work on it, and this cut's share of the joining.
+        if (lane == 0) {
+            int4 a = make_int4(-1, 0, 0, 0), b = make_int4(0, 0, 0, 0);
+            if (x0 < x1) {
+                ExUnit U;
+                ex_unit<C::TQ>(P, cum, x0, U);
+                if (U.first < x0) {
+                    const int c0 = static_cast<int>(ex_owner(U.first, all, ctas));
+                    const int c1 = static_cast<int>(ex_owner(U.first + U.tiles - 1, all, ctas));
+                    // c0's partial: its last segment, slot 1 unless also its first
+                    const int slot0 = ex_start(c0, all, ctas) >= U.first ? 0 : 1;
+                    a = make_int4(U.qrow, U.g, U.tvalid, slot0);
+                    b = make_int4(c0, c1, static_cast<int>(blockIdx.x) - c0 - 1, c1 - c0);
+                }
+            }
+            P.ws_rec[2 * blockIdx.x] = a;
+            P.ws_rec[2 * blockIdx.x + 1] = b;
+        }
+        __syncwarp();
     } else if (warp == EX_WARP_MMA) {
         // ------------------------------------------------------ UMMA issuer
         if (lane == 0 && x0 < x1) {
@@ -524,6 +539,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                         ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
                                        SITE_EX_MMA);
                         if (!ok) break;
+                        fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = k_lo0 + slot * (C::SLOT_BYTES >> 4);
 #pragma unroll
@@ -549,6 +565,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                         ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
                                        SITE_EX_MMA);
                         if (!ok) break;
+                        fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = v_lo0 + slot * (C::SLOT_BYTES >> 4);
 #pragma unroll
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         const uint32_t p_word = smem_u32(sP) + (key_l >> 6) * (R * 128) + (key_l & 62) * 2;
         const bool odd = lane & 1;
         bool ok = true;
-        uint32_t unit = 0;
+        uint32_t unit = 0, raises = 0;
         long long x = x0;
         while (x < x1 && ok) {
             ExUnit U;
@@ -592,7 +609,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
 #pragma unroll
             for (int c = 0; c < HC; ++c) {
                 l32[c] = lr[c] = 0.f;
-                m[c] = -INFINITY;
+                m[c] = EX_NO_MAX;
             }
             for (int t = t_begin; t < t_end; ++t) {
                 const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
@@ -603,17 +620,38 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                 tc_fence_after();
                 float p[HC];
                 ex_tmem_ld<HC>(s_addr + b * R, p);
-                const int key = U.lo + t * EX_BN + key_l;
-                // every row sees every key of an inner tile
                 const int k0 = U.lo + t * EX_BN;
+                const int key = k0 + key_l;
+                // an inner tile is seen whole by every row
                 const bool edge = k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
                                   (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window);
+                // p: scores in log2 units, less the fixed shift
                 if (FIX || P.has_cap) {
-                    // cap in log2 units, minus the fixed shift
-                    const float sh = FIX ? P.cap_l2 - P.fixed_ref : P.cap_l2;
+                    const float sh = FIX ? -P.fixed_ref : 0.f;
+                    float ax = 0.f;
 #pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        p[c] = fmaf(-2.0f * P.cap_l2, rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)), sh);
+                    for (int c = 0; c < HC; c += 2) ax = fmax3f(ax, fabsf(p[c]), fabsf(p[c + 1]));
+                    if (__all_sync(0xffffffffu, ax <= P.series_max)) {
+                        // tanh's series, two rows per instruction
+                        const float2 s0 = make_float2(P.series[0], P.series[0]);
+                        const float2 s1 = make_float2(P.series[1], P.series[1]);
+                        const float2 s2 = make_float2(P.series[2], P.series[2]);
+                        const float2 s3 = make_float2(P.series[3], P.series[3]);
+#pragma unroll
+                        for (int c = 0; c < HC; c += 2) {
+                            const float2 v = make_float2(p[c], p[c + 1]);
+                            const float2 v2 = mul2(v, v);
+                            const float2 h = fma2(v2, fma2(v2, fma2(v2, s3, s2), s1), s0);
+                            const float2 y = fma2(v, h, make_float2(sh, sh));
+                            p[c] = y.x;
+                            p[c + 1] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < HC; ++c)
+                            p[c] = fmaf(-2.0f * P.cap_l2,
+                                        rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)), P.cap_l2 + sh);
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < HC; ++c) p[c] *= P.scale_l2;
@@ -627,67 +665,76 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                     }
                 }
                 if constexpr (!FIX) {
-                    float mx[HC];
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) mx[c] = p[c];
-                    const float w = ex_reduce<HC, true>(mx);
-                    float* st = s_max + ((it & 1) * 2 + wg) * 4 * HC;
-                    if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
-                    mbar_arrive(&wg_max[wg]);
-                    ok = mbar_wait(&wg_max[wg], it & 1, abort_flag, lim, SITE_EX_SM);
+                    for (int c = 0; c < HC; c += 2)
+                        top = fmax3f(top, p[c] - m[c], p[c + 1] - m[c + 1]);
+                    const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
+                    volatile uint32_t* vote = votes + (b * 2 + wg);
+                    if (lane == 0) {
+                        reinterpret_cast<volatile unsigned char*>(vote)[qd] = raise;
+                        mbar_arrive(&wg_vote[wg]);
+                    }
+                    ok = mbar_wait(&wg_vote[wg], it & 1, abort_flag, lim, SITE_EX_SM);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    bool grow = false, any = false;
-                    float nm[HC];
+                    if (*vote != 0) {  // the same decision in the whole warpgroup
+                        float* st = s_max + ((raises & 1) * 2 + wg) * 4 * HC;
+                        volatile float* fac = s_fac + ((raises & 1) * 2 + wg) * HC;
+                        float mx[HC];
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        nm[c] = fmaxf(fmaxf(st[c], st[HC + c]), fmaxf(st[2 * HC + c], st[3 * HC + c]));
-                        // a row's first finite max needs no rescaling, its O is zero
-                        any |= nm[c] > m[c];
-                        grow |= nm[c] > m[c] + EX_RESCALE_LOG2 && m[c] != -INFINITY;
-                    }
-                    // (the same decision in all threads of the warpgroup)
-                    if (grow && t > t_begin) {
-                        const uint32_t pv = it - 1;  // O must hold every tile before this
-                        ok = mbar_wait(&p_empty[pv & 1], (pv >> 1) & 1, abort_flag, lim, SITE_EX_SM);
+                        for (int c = 0; c < HC; ++c) mx[c] = p[c];
+                        const float w = ex_reduce<HC, true>(mx);
+                        if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
+                        mbar_arrive(&wg_max[wg]);
+                        ok = mbar_wait(&wg_max[wg], raises & 1, abort_flag, lim, SITE_EX_SM);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        tc_fence_after();
+                        ++raises;
+                        if (t > t_begin) {  // O must hold every tile before this
+                            const uint32_t pv = it - 1;
+                            ok = mbar_wait(&p_empty[pv & 1], (pv >> 1) & 1, abort_flag, lim,
+                                           SITE_EX_SM);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
 #pragma unroll
                         for (int c = 0; c < HC; ++c) {
-                            const float n = fmaxf(m[c], nm[c]);
-                            const float f = m[c] == -INFINITY ? 1.0f : ex2_approx(m[c] - n);
+                            const float n = fmaxf(fmaxf(m[c], st[c]),
+                                                  fmax3f(st[HC + c], st[2 * HC + c], st[3 * HC + c]));
+                            // factor of what was summed so far (0 where nothing was),
+                            // parked in shared memory (every thread writes the same)
+                            const float f = ex2_approx(m[c] - n);
                             m[c] = n;
                             l32[c] *= f;
                             lr[c] *= f;
-                            nm[c] = f;
+                            fac[c] = f;
                         }
+                        if (t > t_begin) {
 #pragma unroll
-                        for (int o = 0; o < C::O_BLOCKS; ++o) {
-                            float a[HC];
-                            ex_tmem_ld<HC>(o_addr + o * R, a);
+                            for (int o = 0; o < C::O_BLOCKS; ++o) {
+                                float a[HC];
+                                ex_tmem_ld<HC>(o_addr + o * R, a);
 #pragma unroll
-                            for (int c = 0; c < HC; ++c) a[c] *= nm[c];
-                            ex_tmem_st<HC>(o_addr + o * R, a);
+                                for (int c = 0; c < HC; ++c) a[c] *= fac[c];
+                                ex_tmem_st<HC>(o_addr + o * R, a);
+                            }
+                            tmem_wait_st();
                         }
-                        tmem_wait_st();
-                    } else if (any) {
-#pragma unroll
-                        for (int c = 0; c < HC; ++c)
-                            if (m[c] == -INFINITY) m[c] = nm[c];
                     }
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) p[c] -= m[c] == -INFINITY ? 0.f : m[c];
-                }
-                if (it >= 2) {  // P buffer: the product of tile it - 2 has read it
-                    ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    for (int c = 0; c < HC; ++c) p[c] -= m[c];
                 }
 #pragma unroll
                 for (int c = 0; c < HC; ++c) {
                     p[c] = ex2_approx(p[c]);
                     l32[c] += p[c];
+                }
+                if (it >= 2) {  // P buffer: the product of tile it - 2 has read it
+                    ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                 }
                 // rows c and c + 4: lanes 2j, 2j+1 swap halves and store the key
                 // pair of one row each (a warp's store hits every bank once)
@@ -757,7 +804,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             }
             if (key_l < HC && wg * HC + key_l < rows) {
                 const int r = wg * HC + key_l;
-                float a = 0.f, l = 0.f, mm = FIX ? P.fixed_ref : -INFINITY;
+                float a = 0.f, l = 0.f, mm = FIX ? P.fixed_ref : EX_NO_MAX;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     a += ssum[(w * HC + key_l) * 2];
@@ -789,58 +836,72 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
     if (warp == EX_WARP_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// Joins the partial results of units that more than one CTA worked on. CTA c
-// looks at the start of stretch c + 1: where that cuts a unit, the unit's n
-// cuts share its rows and columns between them.
-//   M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
+// Joins the partial results of units that more than one CTA worked on. Where
+// the stretch of CTA blockIdx.x + 1 starts inside a unit, that CTA's record
+// says which partials the unit has; the cuts of a unit share its rows. A warp
+// takes a row (128 columns of it at d = 256): M = max m_i,
+//   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
 template <int D, int R>
-__global__ void __launch_bounds__(256) extend_merge(const ExParams P, int grid) {
-    using C = ExCfg<D, R>;
-    __shared__ long long cum[EX_MAX_SEQS + 1];
-    ex_cum<C::TQ>(P, cum);
-    const long long all = cum[P.num_seqs];
-    const long long ctas = ex_ctas(P, all, grid);
-    const long long cut = blockIdx.x + 1ll;
+__global__ void __launch_bounds__(256) extend_merge(const ExParams P) {
+    constexpr int VW = D == 64 ? 2 : 4;           // columns per lane
+    constexpr int BLK = D / (32 * VW);            // column blocks of a row
+    __shared__ float weight[8][EX_MAX_CTAS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (cut >= ctas) return;
-    const long long x = ex_start(cut, all, ctas);
-    ExUnit U;
-    ex_unit<C::TQ>(P, cum, x, U);
-    if (U.first == x) return;
-    const int c0 = static_cast<int>(ex_owner(U.first, all, ctas));
-    const int c1 = static_cast<int>(ex_owner(U.first + U.tiles - 1, all, ctas));
-    const int share = static_cast<int>(cut) - c0 - 1, shares = c1 - c0;
-    // the unit is its first CTA's last segment (slot 1 unless it is also its
-    // first) and every other CTA's first
-    const bool c0_first = ex_start(c0, all, ctas) >= U.first;
-    const int n = 2 * U.tvalid * (D / 4);
-    for (int e = share * 256 + threadIdx.x; e < n; e += shares * 256) {
-        const int r = e / (D / 4), c = e % (D / 4);
+    const int4 ra = P.ws_rec[2 * (blockIdx.x + 1)], rb = P.ws_rec[2 * (blockIdx.x + 1) + 1];
+    if (ra.x < 0) return;
+    const int qrow0 = ra.x, g = ra.y, rows = 2 * ra.z;
+    const int c0 = rb.x, parts = rb.y - rb.x + 1, share = rb.z, shares = rb.w;
+    float* w = weight[warp];
+    // partial i is slot 0 of CTA c0 + i, but for c0's own
+    auto slot = [&](int i) -> size_t {
+        return static_cast<size_t>(c0 + i) * 2 + (i == 0 ? ra.w : 0);
+    };
+    for (int e = share * 8 + warp; e < rows * BLK; e += shares * 8) {
+        const int r = e / BLK, col = (e % BLK) * 32 * VW + lane * VW;
         float M = -INFINITY;
-        for (int i = c0; i <= c1; ++i) {
-            const size_t ws = static_cast<size_t>(i) * 2 + (i == c0 && !c0_first ? 1 : 0);
-            M = fmaxf(M, P.ws_s[(ws * R + r) * 4]);
+        for (int i = lane; i < parts; i += 32) {
+            w[i] = P.ws_s[(slot(i) * R + r) * 4];
+            M = fmaxf(M, w[i]);
         }
-        const float Mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float a = 0.f, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = c0; i <= c1; ++i) {
-            const size_t ws = static_cast<size_t>(i) * 2 + (i == c0 && !c0_first ? 1 : 0);
-            const float4 st = *reinterpret_cast<const float4*>(P.ws_s + (ws * R + r) * 4);
-            const float4 v = *reinterpret_cast<const float4*>(P.ws_o + (ws * R + r) * D + 4 * c);
-            const float w = ex2_approx(st.x - Mu);
-            a = fmaf(w, st.y, a);
-            l = fmaf(w, st.z, l);
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
+        for (int i = lane; i < parts; i += 32) {
+            const float* st = P.ws_s + (slot(i) * R + r) * 4;
+            w[i] = ex2_approx(w[i] - M);
+            a = fmaf(w[i], st[1], a);
+            l = fmaf(w[i], st[2], l);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+        }
+        __syncwarp();
+        float acc[VW];
+#pragma unroll
+        for (int k = 0; k < VW; ++k) acc[k] = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+            const float* o = P.ws_o + (slot(i) * R + r) * D + col;
+            float v[VW];
+            if constexpr (VW == 4)
+                *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+            else
+                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+#pragma unroll
+            for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[i], v[k], acc[k]);
+        }
+        __syncwarp();  // w is written anew for the next row
         const float inv = l > 0.f ? 1.0f / l : 0.f;
-        const int qrow = U.qrow + (r >> 1), h = 2 * U.g + (r & 1);
-        *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(qrow) * P.H + h) * D + 4 * c) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (c == 0 && P.lse != nullptr)
+        const int qrow = qrow0 + (r >> 1), h = 2 * g + (r & 1);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            P.out + (static_cast<size_t>(qrow) * P.H + h) * D + col);
+#pragma unroll
+        for (int k = 0; k < VW / 2; ++k)
+            dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+        if (e % BLK == 0 && lane == 0 && P.lse != nullptr)
             P.lse[static_cast<size_t>(h) * P.total_q + qrow] =
                 a > 0.f ? (M + log2f(a)) * 0.69314718055994531f : -INFINITY;
     }
