@@ -78,7 +78,7 @@ struct ExCfg {
     // tiles after the ring must span that
     static constexpr int PAD = D == 64 && FIXED < CH_BYTES ? CH_BYTES - FIXED : 0;
     static constexpr int CUM_BYTES = 8 * (EX_MAX_SEQS + 1);
-    static constexpr int CTRL_BYTES = 320 + 2 * 2 * 4 * HC * 12 + 2 * 2 * HC * 4;
+    static constexpr int CTRL_BYTES = 320 + 2 * 2 * 4 * HC * 12 + (8 + 4) * HC * 4;
     static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - PAD - CUM_BYTES - CTRL_BYTES - 64;
     static constexpr int NS_FIT = BUDGET / SLOT_BYTES;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
     // [warp][HC], sums [unit parity][..][..][HC][2]
     float* s_max = reinterpret_cast<float*>(bars + 40);
     float* s_sum = s_max + 2 * 2 * 4 * HC;
-    float* s_fac = s_sum + 2 * 2 * 4 * HC * 2;  // [exchange parity][warpgroup][HC]
+    float* s_fac = s_sum + 2 * 2 * 4 * HC * 2;  // factors of a raise [warp][HC]
+    float* s_ref = s_fac + 8 * HC;              // references [buffer][warpgroup][HC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = P.timeout_ns;
@@ -593,11 +594,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
         const uint32_t s_addr = tmem + lane_addr + wg * HC;
         const uint32_t o_addr = tmem + lane_addr + 2 * R + wg * HC;
-        // P: row r, this thread's pair of keys (even, odd): one 32-bit word
-        const uint32_t p_word = smem_u32(sP) + (key_l >> 6) * (R * 128) + (key_l & 62) * 2;
+        // P: row r, this thread's pair of keys (even, odd): one 32-bit word.
+        // Even lanes store rows c8 + 0..3, odd lanes rows c8 + 4..7; a row's
+        // swizzle depends on r mod 8 only, so four addresses serve every c8.
         const bool odd = lane & 1;
+        uint32_t p_addr[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r8 = k + (odd ? 4 : 0);
+            p_addr[k] = (smem_u32(sP) + (key_l >> 6) * (R * 128) + (wg * HC + r8) * 128 +
+                         (key_l & 62) * 2) ^ (r8 << 4);
+        }
         bool ok = true;
-        uint32_t unit = 0, raises = 0;
+        uint32_t unit = 0, raises = 0, refs = 0;
+        float* m = nullptr;  // this warpgroup's references, in shared memory
         long long x = x0;
         while (x < x1 && ok) {
             ExUnit U;
@@ -605,11 +615,13 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             const long long end = U.first + U.tiles;
             const int t_begin = static_cast<int>(x - U.first);
             const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
-            float l32[HC], lr[HC], m[HC];
+            float l32[HC], lr[HC];
 #pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                l32[c] = lr[c] = 0.f;
-                m[c] = EX_NO_MAX;
+            for (int c = 0; c < HC; ++c) l32[c] = lr[c] = 0.f;
+            if constexpr (!FIX) {
+                m = s_ref + ((++refs & 1) * 2 + wg) * HC;
+                if (lane < HC) m[lane] = EX_NO_MAX;  // all four warps write the same
+                __syncwarp();
             }
             for (int t = t_begin; t < t_end; ++t) {
                 const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
@@ -667,8 +679,11 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                 if constexpr (!FIX) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < HC; c += 2)
-                        top = fmax3f(top, p[c] - m[c], p[c + 1] - m[c + 1]);
+                    for (int c = 0; c < HC; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(m + c);
+                        top = fmax3f(top, p[c] - f.x, p[c + 1] - f.y);
+                        top = fmax3f(top, p[c + 2] - f.z, p[c + 3] - f.w);
+                    }
                     const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
                     volatile uint32_t* vote = votes + (b * 2 + wg);
                     if (lane == 0) {
@@ -680,17 +695,37 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                     if (!ok) break;
                     if (*vote != 0) {  // the same decision in the whole warpgroup
                         float* st = s_max + ((raises & 1) * 2 + wg) * 4 * HC;
-                        volatile float* fac = s_fac + ((raises & 1) * 2 + wg) * HC;
-                        float mx[HC];
+                        {
+                            float mx[HC];
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) mx[c] = p[c];
-                        const float w = ex_reduce<HC, true>(mx);
-                        if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
+                            for (int c = 0; c < HC; ++c) mx[c] = p[c];
+                            const float w = ex_reduce<HC, true>(mx);
+                            if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
+                        }
                         mbar_arrive(&wg_max[wg]);
                         ok = mbar_wait(&wg_max[wg], raises & 1, abort_flag, lim, SITE_EX_SM);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         ++raises;
+                        // new references into the other buffer (the other warps
+                        // may still read this one), and the factors of what was
+                        // summed so far (0 where nothing was)
+                        float* next = s_ref + ((++refs & 1) * 2 + wg) * HC;
+                        float* fac = s_fac + (warp * HC);
+                        if (lane < HC) {
+                            const float n = fmaxf(fmaxf(m[lane], st[lane]),
+                                                  fmax3f(st[HC + lane], st[2 * HC + lane],
+                                                         st[3 * HC + lane]));
+                            next[lane] = n;
+                            fac[lane] = ex2_approx(m[lane] - n);
+                        }
+                        m = next;
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) {
+                            l32[c] *= fac[c];
+                            lr[c] *= fac[c];
+                        }
                         if (t > t_begin) {  // O must hold every tile before this
                             const uint32_t pv = it - 1;
                             ok = mbar_wait(&p_empty[pv & 1], (pv >> 1) & 1, abort_flag, lim,
@@ -698,33 +733,29 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                             tc_fence_after();
-                        }
-#pragma unroll
-                        for (int c = 0; c < HC; ++c) {
-                            const float n = fmaxf(fmaxf(m[c], st[c]),
-                                                  fmax3f(st[HC + c], st[2 * HC + c], st[3 * HC + c]));
-                            // factor of what was summed so far (0 where nothing was),
-                            // parked in shared memory (every thread writes the same)
-                            const float f = ex2_approx(m[c] - n);
-                            m[c] = n;
-                            l32[c] *= f;
-                            lr[c] *= f;
-                            fac[c] = f;
-                        }
-                        if (t > t_begin) {
 #pragma unroll
                             for (int o = 0; o < C::O_BLOCKS; ++o) {
-                                float a[HC];
-                                ex_tmem_ld<HC>(o_addr + o * R, a);
 #pragma unroll
-                                for (int c = 0; c < HC; ++c) a[c] *= fac[c];
-                                ex_tmem_st<HC>(o_addr + o * R, a);
+                                for (int c8 = 0; c8 < HC; c8 += 8) {
+                                    float a[8];
+                                    ex_tmem_ld<8>(o_addr + o * R + c8, a);
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c) a[c] *= fac[c8 + c];
+                                    ex_tmem_st<8>(o_addr + o * R + c8, a);
+                                }
                             }
                             tmem_wait_st();
                         }
+                        __syncwarp();  // fac is read before the next raise writes it
                     }
 #pragma unroll
-                    for (int c = 0; c < HC; ++c) p[c] -= m[c];
+                    for (int c = 0; c < HC; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(m + c);
+                        p[c] -= f.x;
+                        p[c + 1] -= f.y;
+                        p[c + 2] -= f.z;
+                        p[c + 3] -= f.w;
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < HC; ++c) {
@@ -748,9 +779,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
                         const uint32_t w = odd ? __byte_perm(got, own, 0x7632)
                                                : __byte_perm(own, got, 0x5410);
-                        const int r = wg * HC + c + (odd ? 4 : 0);
-                        const uint32_t a = (p_word + b * C::P_BYTES + r * 128) ^ ((r & 7) << 4);
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(
+                                         p_addr[c - c8] + b * C::P_BYTES + c8 * 128),
+                                     "r"(w)
+                                     : "memory");
                     }
                 }
                 fence_async_smem();
@@ -810,11 +842,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                     a += ssum[(w * HC + key_l) * 2];
                     l += ssum[(w * HC + key_l) * 2 + 1];
                 }
-                if constexpr (!FIX) {
-#pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        if (c == key_l) mm = m[c];
-                }
+                if constexpr (!FIX) mm = m[key_l];
                 if (!whole) {
                     float* s = P.ws_s + (ws * R + r) * 4;
                     s[0] = mm;
