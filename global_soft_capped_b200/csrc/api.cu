@@ -643,7 +643,7 @@ int launch_extend(g2::ExParams& P, cudaStream_t stream) {
         cudaSuccess)
         return G2ATTN_ERR_CUDA;
     const int grid = std::min(sms, g2::EX_MAX_CTAS);
-    kern<<<grid, g2::EX_THREADS, C::SMEM_BYTES, stream>>>(P);
+    kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(P);
     if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
     if (grid == 1) return G2ATTN_OK;  // nothing to join
     // the merge's prologue overlaps the attention kernel's end

@@ -24,17 +24,18 @@
 // sums) in the workspace, at most two per CTA, and extend_merge joins them in
 // the order of the keys (no atomics: results do not depend on timing).
 //
-// One CTA of 384 threads per SM:
-//   warps 0..7   softmax: warpgroup w/4 takes rows w/4*R/2 .. of S^T, thread =
+// One CTA per SM, warps in this order:
+//   softmax      2 warpgroups (R = 64: 4, so that enough warps hide each other's
+//                latencies), each with its R / 2 (R / 4) rows of S^T, thread =
 //                key; writes P as bf16 into shared memory; at a unit's end
 //                reads O^T (lane = d column) and writes out or the partial.
-//   warp 8       tensor memory, one thread issues the UMMAs.
-//   warps 9, 10  producers: 16-byte asynchronous copies of Q, K and V rows into
-//                128-byte-swizzled tiles. Each row's page is looked up, so
-//                pages may be of any size; rows behind the last visible key
-//                are filled with zeros (what the cache holds there, NaN
-//                included, does not matter).
-//   warp 11      writes the CTA's merge record.
+//   1 warp       tensor memory, one thread issues the UMMAs.
+//   2 producers  16-byte asynchronous copies of Q, K and V rows into 128-byte-
+//                swizzled tiles, counted on the slots' barriers. Each row's
+//                page is looked up, so pages may be of any size; rows behind the
+//                last visible key are filled with zeros (what the cache holds
+//                there, NaN included, does not matter).
+//   1 warp       writes the CTA's merge record.
 // Softmax: fp32, log2 domain. With the cap the prefill's fixed shift where it
 // fits. Else a reference per row that is the row's maximum over its first tile
 // and is only raised (and O and the sums rescaled) when a score passes it by
@@ -50,12 +51,7 @@
 namespace g2 {
 
 constexpr int EX_BN = 128;            // keys per tile
-constexpr int EX_SM_THREADS = 256;    // softmax warps 0..7
-constexpr int EX_WARP_MMA = 8;
-constexpr int EX_WARP_PROD = 9;
 constexpr int EX_PROD_WARPS = 2;
-constexpr int EX_WARP_RECORD = 11;
-constexpr int EX_THREADS = 384;       // 12 warps: up to 168 registers per thread
 constexpr int EX_MAX_SEQS = 1024;     // per-launch table in shared memory
 constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
 constexpr float EX_RAISE_LOG2 = 64.0f;   // see the softmax above
@@ -64,7 +60,13 @@ constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key y
 template <int D, int R>
 struct ExCfg {
     static constexpr int TQ = R / 2;                      // positions per unit
-    static constexpr int HC = R / 2;                      // rows per softmax warpgroup
+    static constexpr int NWG = R == 64 ? 4 : 2;           // softmax warpgroups
+    static constexpr int HC = R / NWG;                    // rows per softmax warpgroup
+    static constexpr int SM_WARPS = 4 * NWG;
+    static constexpr int WARP_MMA = SM_WARPS;
+    static constexpr int WARP_PROD = SM_WARPS + 1;
+    static constexpr int WARP_RECORD = WARP_PROD + EX_PROD_WARPS;
+    static constexpr int THREADS = 32 * (WARP_RECORD + 1);  // 384 or 640
     static constexpr int SLOT_COLS = D < 128 ? D : 128;   // d columns of a slot
     static constexpr int SLOT_BYTES = EX_BN * SLOT_COLS * 2;
     static constexpr int KSL = D / SLOT_COLS;             // slots per K (or V) tile
@@ -78,7 +80,7 @@ struct ExCfg {
     // tiles after the ring must span that
     static constexpr int PAD = D == 64 && FIXED < CH_BYTES ? CH_BYTES - FIXED : 0;
     static constexpr int CUM_BYTES = 8 * (EX_MAX_SEQS + 1);
-    static constexpr int CTRL_BYTES = 320 + 2 * 2 * 4 * HC * 12 + (8 + 4) * HC * 4;
+    static constexpr int CTRL_BYTES = 448 + 30 * R * 4;
     static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - PAD - CUM_BYTES - CTRL_BYTES - 64;
     static constexpr int NS_FIT = BUDGET / SLOT_BYTES;
     static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
@@ -312,9 +314,68 @@ __device__ __forceinline__ int ex_col(int lane) {
     return N == 32 ? lane : (N == 16 ? lane >> 1 : lane >> 2);
 }
 
+// Scores in log2 units, less the fixed shift, of this lane's key and HC rows, from the
+// raw products in TMEM.
+template <int HC, bool FIX>
+__device__ __forceinline__ void ex_scores(const ExParams& P, uint32_t addr, float (&p)[HC]) {
+    ex_tmem_ld<HC>(addr, p);
+    if (FIX || P.has_cap) {
+        const float sh = FIX ? -P.fixed_ref : 0.f;
+        float ax = 0.f;
+#pragma unroll
+        for (int c = 0; c < HC; c += 2) ax = fmax3f(ax, fabsf(p[c]), fabsf(p[c + 1]));
+        if (__all_sync(0xffffffffu, ax <= P.series_max)) {
+            // tanh's series, two rows per instruction
+            const float2 s0 = make_float2(P.series[0], P.series[0]);
+            const float2 s1 = make_float2(P.series[1], P.series[1]);
+            const float2 s2 = make_float2(P.series[2], P.series[2]);
+            const float2 s3 = make_float2(P.series[3], P.series[3]);
+#pragma unroll
+            for (int c = 0; c < HC; c += 2) {
+                const float2 v = make_float2(p[c], p[c + 1]);
+                const float2 v2 = mul2(v, v);
+                const float2 h = fma2(v2, fma2(v2, fma2(v2, s3, s2), s1), s0);
+                const float2 y = fma2(v, h, make_float2(sh, sh));
+                p[c] = y.x;
+                p[c + 1] = y.y;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < HC; ++c)
+                p[c] = fmaf(-2.0f * P.cap_l2, rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)),
+                            P.cap_l2 + sh);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < HC; c += 2) {
+            const float2 y = mul2(make_float2(p[c], p[c + 1]), make_float2(P.scale_l2, P.scale_l2));
+            p[c] = y.x;
+            p[c + 1] = y.y;
+        }
+    }
+}
+
+// p += the negated references of the HC rows; returns the largest result.
+template <int HC>
+__device__ __forceinline__ float ex_less_ref(const float* neg, float (&p)[HC]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < HC; c += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(neg + c);
+        const float2 a = add2(make_float2(p[c], p[c + 1]), make_float2(f.x, f.y));
+        const float2 b = add2(make_float2(p[c + 2], p[c + 3]), make_float2(f.z, f.w));
+        p[c] = a.x;
+        p[c + 1] = a.y;
+        p[c + 2] = b.x;
+        p[c + 3] = b.y;
+        top = fmax3f(top, fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+    }
+    return top;
+}
+
 // SM = PF_SM_FIXED or PF_SM_CAP (any running max; has_cap tells the cap).
 template <int D, int R, int SM>
-__global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) {
+__global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const ExParams P) {
     using C = ExCfg<D, R>;
     constexpr int HC = C::HC;
     constexpr bool FIX = SM == PF_SM_FIXED;
@@ -334,20 +395,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
     uint64_t* p_full = bars + 20;          // [2]
     uint64_t* p_empty = bars + 22;         // [2]
     uint64_t* o_full = bars + 24;
-    uint64_t* wg_max = bars + 25;          // [2] warpgroup exchanges
-    uint64_t* wg_sum = bars + 27;          // [2]
-    uint64_t* drain = bars + 29;
-    uint64_t* wg_vote = bars + 30;         // [2]
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 32);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 33);
+    uint64_t* drain = bars + 25;
+    uint64_t* wg_max = bars + 26;          // [4] warpgroup exchanges
+    uint64_t* wg_sum = bars + 30;          // [4]
+    uint64_t* wg_vote = bars + 34;         // [4]
     // votes of the warps of a warpgroup, a byte each [tile parity][warpgroup]
-    volatile uint32_t* votes = reinterpret_cast<volatile uint32_t*>(bars + 34);
+    volatile uint32_t* votes = reinterpret_cast<volatile uint32_t*>(bars + 40);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 44);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 45);
     // row statistics that they exchange: maxima [exchange parity][warpgroup]
     // [warp][HC], sums [unit parity][..][..][HC][2]
-    float* s_max = reinterpret_cast<float*>(bars + 40);
-    float* s_sum = s_max + 2 * 2 * 4 * HC;
-    float* s_fac = s_sum + 2 * 2 * 4 * HC * 2;  // factors of a raise [warp][HC]
-    float* s_ref = s_fac + 8 * HC;              // references [buffer][warpgroup][HC]
+    float* s_max = reinterpret_cast<float*>(bars + 48);
+    float* s_sum = s_max + 8 * R;
+    float* s_fac = s_sum + 16 * R;  // factors of a raise [warp][HC]
+    float* s_ref = s_fac + 4 * R;   // negated references [buffer][warpgroup][HC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = P.timeout_ns;
@@ -359,8 +420,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], EX_SM_THREADS);
+            mbar_init(&p_full[i], C::SM_WARPS * 32);
             mbar_init(&p_empty[i], 1);
+        }
+        for (int i = 0; i < C::NWG; ++i) {
             mbar_init(&wg_max[i], 128);
             mbar_init(&wg_vote[i], 4);
             mbar_init(&wg_sum[i], 128);
@@ -370,7 +433,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == EX_WARP_MMA) {
+    if (warp == C::WARP_MMA) {
         tmem_alloc(tmem_ptr, C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -389,12 +452,12 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         x1 = ex_start(blockIdx.x + 1ll, all, ctas);
     }
 
-    if (warp >= EX_WARP_PROD && warp < EX_WARP_RECORD) {
+    if (warp >= C::WARP_PROD && warp < C::WARP_RECORD) {
         // -------------------------------------------------------- producers
         constexpr int RW = EX_BN / EX_PROD_WARPS;  // rows of a tile per warp
         constexpr int RL = RW / 32;                // of which a lane looks up this many
-        const int pw = warp - EX_WARP_PROD;
-        const int pt = tid - EX_WARP_PROD * 32;
+        const int pw = warp - C::WARP_PROD;
+        const int pt = tid - C::WARP_PROD * 32;
         uint32_t fill = 0;                         // slots filled
         bool ok = true;
         auto await = [&](uint64_t* bar, uint32_t parity) {
@@ -480,7 +543,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             g_v = U.g;
         }
         cp_async_wait_all();
-    } else if (warp == EX_WARP_RECORD) {
+    } else if (warp == C::WARP_RECORD) {
         // ----------------------------------------------------- merge record
         // Where this CTA's stretch starts inside a unit: the unit's rows, the
         // CTAs c0 .. c1 that work on it, and this cut's share of the joining.
@@ -502,7 +565,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             P.ws_rec[2 * blockIdx.x + 1] = b;
         }
         __syncwarp();
-    } else if (warp == EX_WARP_MMA) {
+    } else if (warp == C::WARP_MMA) {
         // ------------------------------------------------------ UMMA issuer
         if (lane == 0 && x0 < x1) {
             constexpr uint32_t IDESC_S = idesc_bf16(128, R, false);
@@ -598,6 +661,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         // Even lanes store rows c8 + 0..3, odd lanes rows c8 + 4..7; a row's
         // swizzle depends on r mod 8 only, so four addresses serve every c8.
         const bool odd = lane & 1;
+        const uint32_t p_sel = odd ? 0x3276u : 0x5410u;  // (got, own) high or (own, got) low halves
         uint32_t p_addr[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -607,7 +671,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
         }
         bool ok = true;
         uint32_t unit = 0, raises = 0, refs = 0;
-        float* m = nullptr;  // this warpgroup's references, in shared memory
+        float* neg = nullptr;  // this warpgroup's negated references
         long long x = x0;
         while (x < x1 && ok) {
             ExUnit U;
@@ -615,12 +679,14 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             const long long end = U.first + U.tiles;
             const int t_begin = static_cast<int>(x - U.first);
             const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
-            float l32[HC], lr[HC];
+            // sums of the weights of rows c and c + 4 of every eight: fp32 ones,
+            // and the rounded ones
+            float2 l32[HC / 2], lr[HC / 2];
 #pragma unroll
-            for (int c = 0; c < HC; ++c) l32[c] = lr[c] = 0.f;
+            for (int c = 0; c < HC / 2; ++c) l32[c] = lr[c] = make_float2(0.f, 0.f);
             if constexpr (!FIX) {
-                m = s_ref + ((++refs & 1) * 2 + wg) * HC;
-                if (lane < HC) m[lane] = EX_NO_MAX;  // all four warps write the same
+                neg = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
+                if (lane < HC) neg[lane] = -EX_NO_MAX;  // all four warps write the same
                 __syncwarp();
             }
             for (int t = t_begin; t < t_end; ++t) {
@@ -631,61 +697,25 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                 if (!ok) break;
                 tc_fence_after();
                 float p[HC];
-                ex_tmem_ld<HC>(s_addr + b * R, p);
+                ex_scores<HC, FIX>(P, s_addr + b * R, p);
                 const int k0 = U.lo + t * EX_BN;
                 const int key = k0 + key_l;
                 // an inner tile is seen whole by every row
                 const bool edge = k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
                                   (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window);
-                // p: scores in log2 units, less the fixed shift
-                if (FIX || P.has_cap) {
-                    const float sh = FIX ? -P.fixed_ref : 0.f;
-                    float ax = 0.f;
-#pragma unroll
-                    for (int c = 0; c < HC; c += 2) ax = fmax3f(ax, fabsf(p[c]), fabsf(p[c + 1]));
-                    if (__all_sync(0xffffffffu, ax <= P.series_max)) {
-                        // tanh's series, two rows per instruction
-                        const float2 s0 = make_float2(P.series[0], P.series[0]);
-                        const float2 s1 = make_float2(P.series[1], P.series[1]);
-                        const float2 s2 = make_float2(P.series[2], P.series[2]);
-                        const float2 s3 = make_float2(P.series[3], P.series[3]);
-#pragma unroll
-                        for (int c = 0; c < HC; c += 2) {
-                            const float2 v = make_float2(p[c], p[c + 1]);
-                            const float2 v2 = mul2(v, v);
-                            const float2 h = fma2(v2, fma2(v2, fma2(v2, s3, s2), s1), s0);
-                            const float2 y = fma2(v, h, make_float2(sh, sh));
-                            p[c] = y.x;
-                            p[c + 1] = y.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < HC; ++c)
-                            p[c] = fmaf(-2.0f * P.cap_l2,
-                                        rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)), P.cap_l2 + sh);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) p[c] *= P.scale_l2;
-                }
-                if (edge) {
+                auto mask = [&]() {
 #pragma unroll
                     for (int c = 0; c < HC; ++c) {
                         const int pos = U.p0 + ((wg * HC + c) >> 1);
                         if (key > pos || key >= U.hi || (P.window > 0 && pos - key >= P.window))
                             p[c] = -INFINITY;
                     }
-                }
+                };
+                if (edge) mask();
                 if constexpr (!FIX) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < HC; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(m + c);
-                        top = fmax3f(top, p[c] - f.x, p[c + 1] - f.y);
-                        top = fmax3f(top, p[c + 2] - f.z, p[c + 3] - f.w);
-                    }
+                    const float top = ex_less_ref<HC>(neg, p);
                     const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
-                    volatile uint32_t* vote = votes + (b * 2 + wg);
+                    volatile uint32_t* vote = votes + (b * C::NWG + wg);
                     if (lane == 0) {
                         reinterpret_cast<volatile unsigned char*>(vote)[qd] = raise;
                         mbar_arrive(&wg_vote[wg]);
@@ -694,7 +724,9 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (*vote != 0) {  // the same decision in the whole warpgroup
-                        float* st = s_max + ((raises & 1) * 2 + wg) * 4 * HC;
+                        float* st = s_max + ((raises & 1) * C::NWG + wg) * 4 * HC;
+                        ex_scores<HC, FIX>(P, s_addr + b * R, p);
+                        if (edge) mask();
                         {
                             float mx[HC];
 #pragma unroll
@@ -710,21 +742,25 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                         // new references into the other buffer (the other warps
                         // may still read this one), and the factors of what was
                         // summed so far (0 where nothing was)
-                        float* next = s_ref + ((++refs & 1) * 2 + wg) * HC;
-                        float* fac = s_fac + (warp * HC);
+                        float* next = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
+                        float* fac = s_fac + warp * HC;
                         if (lane < HC) {
-                            const float n = fmaxf(fmaxf(m[lane], st[lane]),
+                            const float m = -neg[lane];
+                            const float n = fmaxf(fmaxf(m, st[lane]),
                                                   fmax3f(st[HC + lane], st[2 * HC + lane],
                                                          st[3 * HC + lane]));
-                            next[lane] = n;
-                            fac[lane] = ex2_approx(m[lane] - n);
+                            next[lane] = -n;
+                            fac[lane] = ex2_approx(m - n);
                         }
-                        m = next;
+                        neg = next;
                         __syncwarp();
 #pragma unroll
-                        for (int c = 0; c < HC; ++c) {
-                            l32[c] *= fac[c];
-                            lr[c] *= fac[c];
+                        for (int c = 0; c < HC / 2; ++c) {
+                            const int r = (c >> 2) * 8 + (c & 3);
+                            l32[c].x *= fac[r];
+                            l32[c].y *= fac[r + 4];
+                            lr[c].x *= fac[r];
+                            lr[c].y *= fac[r + 4];
                         }
                         if (t > t_begin) {  // O must hold every tile before this
                             const uint32_t pv = it - 1;
@@ -747,21 +783,11 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                             tmem_wait_st();
                         }
                         __syncwarp();  // fac is read before the next raise writes it
-                    }
-#pragma unroll
-                    for (int c = 0; c < HC; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(m + c);
-                        p[c] -= f.x;
-                        p[c + 1] -= f.y;
-                        p[c + 2] -= f.z;
-                        p[c + 3] -= f.w;
+                        ex_less_ref<HC>(neg, p);
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    p[c] = ex2_approx(p[c]);
-                    l32[c] += p[c];
-                }
+                for (int c = 0; c < HC; ++c) p[c] = ex2_approx(p[c]);
                 if (it >= 2) {  // P buffer: the product of tile it - 2 has read it
                     ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
                     ok = __all_sync(0xffffffffu, ok);
@@ -769,18 +795,18 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                 }
                 // rows c and c + 4: lanes 2j, 2j+1 swap halves and store the key
                 // pair of one row each (a warp's store hits every bank once)
+                const uint32_t p_buf = b * C::P_BYTES;
 #pragma unroll
                 for (int c8 = 0; c8 < HC; c8 += 8) {
 #pragma unroll
-                    for (int c = c8; c < c8 + 4; ++c) {
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = c8 + k, i = c8 / 2 + k;
                         const uint32_t own = pack_bf16x2(p[c], p[c + 4]);
-                        lr[c] += __uint_as_float(own << 16);
-                        lr[c + 4] += __uint_as_float(own & 0xFFFF0000u);
+                        l32[i] = add2(l32[i], make_float2(p[c], p[c + 4]));
+                        lr[i] = add_bf16x2_f32(lr[i], own);
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
-                        const uint32_t w = odd ? __byte_perm(got, own, 0x7632)
-                                               : __byte_perm(own, got, 0x5410);
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(
-                                         p_addr[c - c8] + b * C::P_BYTES + c8 * 128),
+                        const uint32_t w = __byte_perm(own, got, p_sel);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_addr[k] + p_buf + c8 * 128),
                                      "r"(w)
                                      : "memory");
                     }
@@ -791,10 +817,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
             }
             if (!ok) break;
             // row sums over the 128 keys' threads
-            float* ssum = s_sum + ((unit & 1) * 2 + wg) * 4 * HC * 2;
+            float* ssum = s_sum + ((unit & 1) * C::NWG + wg) * 4 * HC * 2;
             {
-                const float a = ex_reduce<HC, false>(l32);
-                const float r = ex_reduce<HC, false>(lr);
+                float v[HC];
+                auto spread = [&](const float2 (&l)[HC / 2]) {
+#pragma unroll
+                    for (int c = 0; c < HC / 2; ++c) {
+                        v[(c >> 2) * 8 + (c & 3)] = l[c].x;
+                        v[(c >> 2) * 8 + (c & 3) + 4] = l[c].y;
+                    }
+                };
+                spread(l32);
+                const float a = ex_reduce<HC, false>(v);
+                spread(lr);
+                const float r = ex_reduce<HC, false>(v);
                 if ((lane & (32 / HC - 1)) == 0) {
                     ssum[(qd * HC + ex_col<HC>(lane)) * 2] = a;
                     ssum[(qd * HC + ex_col<HC>(lane)) * 2 + 1] = r;
@@ -842,7 +878,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
                     a += ssum[(w * HC + key_l) * 2];
                     l += ssum[(w * HC + key_l) * 2 + 1];
                 }
-                if constexpr (!FIX) mm = m[key_l];
+                if constexpr (!FIX) mm = -neg[key_l];
                 if (!whole) {
                     float* s = P.ws_s + (ws * R + r) * 4;
                     s[0] = mm;
@@ -861,7 +897,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1) extend_sm100(const ExParams P) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == EX_WARP_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == C::WARP_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 // Joins the partial results of units that more than one CTA worked on. Where
