@@ -629,28 +629,19 @@ def rope_plan(rotary_dim, *, interleaved=False, device="cuda", frequencies=None,
     return RopePlan(freqs, int(rotary_dim), bool(interleaved), m if mscale is None else mscale)
 
 
-class _on:
-    """The device of a tensor made current for a call (nothing when it is)."""
-    __slots__ = ("want", "had")
-
-    def __init__(self, t):
-        self.want = t.device.index
-
-    def __enter__(self):
-        import torch
-        self.had = torch.cuda.current_device()
-        if self.had != self.want:
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.had != self.want:
-            import torch
-            torch.cuda.set_device(self.had)
-
-
-def _raw_stream(stream, device):
+def _launch(name, device, stream, args):
+    """Calls a C entry point with ``args`` and the stream, its device current."""
     import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    if st != G2ATTN_OK:
+        raise G2AttnError(st, name)
 
 
 def _heads(name, t, device=None):
@@ -675,6 +666,22 @@ def _heads(name, t, device=None):
     if st[-1] != 1 or (H > 1 and st[-2] != d):
         raise ValueError(f"{name}: heads of a token must be dense")
     return n, H, d, step
+
+
+def _used_on(stream, *tensors):
+    """Tensors made here for a call on a stream that is not the current one: their
+    memory is not handed out again before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _dense_like(t):
+    """A new packed tensor of a shape that :func:`_heads` accepted: evenly spaced
+    tokens, for which empty_like's layout is the packed one in the same order."""
+    import torch
+    o = torch.empty_like(t)
+    return o if o.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _ints(name, t, n, device, dtype=None):
@@ -707,22 +714,18 @@ def _rope(q, k, positions, plan, inverse, out, stream):
     if nk != n or dk != d:
         raise ValueError("q and k differ in tokens or head size")
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        qo, ko = _dense_like(q), _dense_like(k)
+        _used_on(stream, qo, ko)
         qos, kos = H * d, Hkv * d
     else:
         qo, ko = out
         if qo.shape != q.shape or ko.shape != k.shape:
             raise ValueError("out: expected the shapes of q and k")
         qos, kos = _heads("out q", qo, q.device)[3], _heads("out k", ko, q.device)[3]
-    with _on(q):
-        st = load_library().g2attn_rope(
-            q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
-            _ints("positions", positions, n, q.device), _plan_args(plan, q.device), n, H, Hkv, d,
-            plan.rotary_dim, int(plan.interleaved), plan.mscale, inverse, qs, ks, qos, kos,
-            _raw_stream(stream, q.device))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_rope")
+    _launch("g2attn_rope", q.device, stream, (
+        q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
+        _ints("positions", positions, n, q.device), _plan_args(plan, q.device), n, H, Hkv, d,
+        plan.rotary_dim, int(plan.interleaved), plan.mscale, inverse, qs, ks, qos, kos))
     return qo, ko
 
 
@@ -738,7 +741,7 @@ def rope_backward(dq, dk, positions, plan, *, out=None, stream=None):
     return _rope(dq, dk, positions, plan, 1, out, stream)
 
 
-def _append(where, q, k, v, cu_seqlens_q, num_seqs, q_out):
+def _append(q, k, v, cu_seqlens_q, num_seqs, q_out, stream):
     """Checks common to the appends: (sizes, strides, q_out, cu pointer)."""
     import torch
     n, H, d, qs = _heads("q", q)
@@ -747,7 +750,8 @@ def _append(where, q, k, v, cu_seqlens_q, num_seqs, q_out):
     if (nk, dk) != (n, d) or (nv, Hv, dv) != (n, Hkv, d):
         raise ValueError("q, k and v differ in tokens, heads or head size")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _dense_like(q)
+        _used_on(stream, q_out)
     elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype != q.dtype \
             or q_out.device != q.device:
         raise ValueError("q_out: expected a contiguous bf16 tensor like q")
@@ -764,18 +768,14 @@ def rope_append(q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, plan, *, 
     """Rotates q (returned) and k and writes k and v to the last rows of every
     sequence of a packed cache (sum L,Hkv,d); cu_seqlens_q None: one token each."""
     n_seqs = cu_seqlens_k.numel() - 1
-    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append", q, k, v, cu_seqlens_q, n_seqs,
-                                                  q_out)
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
     kc = _cache("k_cache", k_cache, q, (None, Hkv, d))
     vc = _cache("v_cache", v_cache, q, tuple(k_cache.shape))
-    with _on(q):
-        st = load_library().g2attn_rope_append(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
-            _ints("cu_seqlens_k", cu_seqlens_k, None, q.device), _plan_args(plan, q.device),
-            n_seqs, n, k_cache.shape[0], H, Hkv, d, plan.rotary_dim, int(plan.interleaved),
-            plan.mscale, qs, ks, vs, _raw_stream(stream, q.device))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_rope_append")
+    _launch("g2attn_rope_append", q.device, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+        _ints("cu_seqlens_k", cu_seqlens_k, None, q.device), _plan_args(plan, q.device), n_seqs, n,
+        k_cache.shape[0], H, Hkv, d, plan.rotary_dim, int(plan.interleaved), plan.mscale, qs, ks,
+        vs))
     return q_out
 
 
@@ -783,18 +783,14 @@ def rope_append_ring(q, k, v, k_ring, v_ring, cu_seqlens_q, seq_lens, plan, *, q
                      stream=None):
     """:func:`rope_append` into ring caches (n,R,Hkv,d); seq_lens with the new tokens."""
     n_seqs = seq_lens.numel()
-    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append_ring", q, k, v, cu_seqlens_q,
-                                                  n_seqs, q_out)
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
     kc = _cache("k_ring", k_ring, q, (n_seqs, None, Hkv, d))
     vc = _cache("v_ring", v_ring, q, tuple(k_ring.shape))
-    with _on(q):
-        st = load_library().g2attn_rope_append_ring(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
-            _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
-            k_ring.shape[1], H, Hkv, d, plan.rotary_dim, int(plan.interleaved), plan.mscale, qs,
-            ks, vs, _raw_stream(stream, q.device))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_rope_append_ring")
+    _launch("g2attn_rope_append_ring", q.device, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+        _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
+        k_ring.shape[1], H, Hkv, d, plan.rotary_dim, int(plan.interleaved), plan.mscale, qs, ks,
+        vs))
     return q_out
 
 
@@ -803,22 +799,17 @@ def rope_append_paged(q, k, v, k_blocks, v_blocks, cu_seqlens_q, block_table, se
     """:func:`rope_append` into paged caches (num_blocks,bs,Hkv,d); block_table
     int32 (n, max_blocks), seq_lens with the new tokens."""
     n_seqs = seq_lens.numel()
-    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append("rope_append_paged", q, k, v, cu_seqlens_q,
-                                                  n_seqs, q_out)
+    n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
     kc = _cache("k_blocks", k_blocks, q, (None, None, Hkv, d))
     vc = _cache("v_blocks", v_blocks, q, tuple(k_blocks.shape))
     if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
         raise ValueError("block_table: expected one row per sequence")
-    with _on(q):
-        st = load_library().g2attn_rope_append_paged(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
-            _ints("block_table", block_table, None, q.device),
-            _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
-            k_blocks.shape[0], k_blocks.shape[1], block_table.shape[1], H, Hkv, d,
-            plan.rotary_dim, int(plan.interleaved), plan.mscale, qs, ks, vs,
-            _raw_stream(stream, q.device))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_rope_append_paged")
+    _launch("g2attn_rope_append_paged", q.device, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
+        _ints("block_table", block_table, None, q.device),
+        _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
+        k_blocks.shape[0], k_blocks.shape[1], block_table.shape[1], H, Hkv, d, plan.rotary_dim,
+        int(plan.interleaved), plan.mscale, qs, ks, vs))
     return q_out
 
 
@@ -846,27 +837,26 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
         raise ValueError("block_table: expected one row per sequence")
     if out is None:
         out = torch.empty_like(q)
+        _used_on(stream, out)
     elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
             or not out.is_contiguous():
         raise ValueError("out: expected a contiguous bf16 tensor like q")
     if lse is None and want_lse:
         lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+        _used_on(stream, lse)
     elif lse is not None and (lse.shape != (H, total_q) or lse.dtype != torch.float32
                               or lse.device != q.device or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous fp32 tensor (H, tokens)")
     if workspace is None:
         workspace = extend_workspace(max_T, d, q.device)
-    with _on(q):
-        st = load_library().g2attn_extend_paged(
-            q.data_ptr(), kc, vc, out.data_ptr(), None if lse is None else lse.data_ptr(),
-            _ints("cu_seqlens_q", cu_seqlens_q, n + 1, q.device),
-            _ints("block_table", block_table, None, q.device),
-            _ints("seq_lens", seq_lens, None, q.device), n, total_q, k_blocks.shape[0],
-            k_blocks.shape[1], block_table.shape[1], int(max_T), H, k_blocks.shape[2], d,
-            query_scale, softcap, int(window), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _raw_stream(stream, q.device))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_extend_paged")
+        _used_on(stream, workspace)
+    _launch("g2attn_extend_paged", q.device, stream, (
+        q.data_ptr(), kc, vc, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        _ints("cu_seqlens_q", cu_seqlens_q, n + 1, q.device),
+        _ints("block_table", block_table, None, q.device),
+        _ints("seq_lens", seq_lens, None, q.device), n, total_q, k_blocks.shape[0],
+        k_blocks.shape[1], block_table.shape[1], int(max_T), H, k_blocks.shape[2], d, query_scale,
+        softcap, int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return out, lse
 
 
@@ -895,13 +885,10 @@ def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, workspace=
     dev = block_table.device
     granted = torch.empty(n, dtype=torch.int32, device=dev)
     ws = pages_workspace(n, nb, dev) if workspace is None else workspace
-    with _on(block_table):
-        st = load_library().g2attn_pages_grow(
-            tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev),
-            granted.data_ptr(), n, nb, int(block_size), cols, ws.data_ptr(),
-            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_pages_grow")
+    _used_on(stream, granted, ws)
+    _launch("g2attn_pages_grow", dev, stream, (
+        tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev), granted.data_ptr(),
+        n, nb, int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
     return granted
 
 
@@ -909,12 +896,9 @@ def pages_truncate(block_table, seq_lens, ref_counts, keep, block_size, *, strea
     """Cuts every sequence to at most keep rows and gives its pages back, in place."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    with _on(block_table):
-        st = load_library().g2attn_pages_truncate(
-            tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("keep", keep, n, dev), n, nb,
-            int(block_size), cols, _raw_stream(stream, dev))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_pages_truncate")
+    _launch("g2attn_pages_truncate", dev, stream, (
+        tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("keep", keep, n, dev), n, nb,
+        int(block_size), cols))
 
 
 def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, workspace=None,
@@ -928,14 +912,11 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
     table = torch.empty_like(block_table)
     lens, src, dst, granted = torch.empty((4, n), dtype=torch.int32, device=dev).unbind(0)
     ws = pages_workspace(n, nb, dev) if workspace is None else workspace
-    with _on(block_table):
-        st = load_library().g2attn_pages_fork(
-            tp, _ints("seq_lens", seq_lens, n, dev), _ints("parents", parents, n, dev),
-            table.data_ptr(), lens.data_ptr(), rp, src.data_ptr(), dst.data_ptr(),
-            granted.data_ptr(), n, nb, int(block_size), cols, ws.data_ptr(),
-            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_pages_fork")
+    _used_on(stream, table, lens, ws)
+    _launch("g2attn_pages_fork", dev, stream, (
+        tp, _ints("seq_lens", seq_lens, n, dev), _ints("parents", parents, n, dev),
+        table.data_ptr(), lens.data_ptr(), rp, src.data_ptr(), dst.data_ptr(), granted.data_ptr(),
+        n, nb, int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
     return table, lens, src, dst, granted
 
 
@@ -948,12 +929,10 @@ def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
     src, dst = torch.empty((2, nb // 2), dtype=torch.int32, device=dev).unbind(0)
     live = torch.empty(1, dtype=torch.int32, device=dev)
     ws = pages_workspace(n, nb, dev) if workspace is None else workspace
-    with _on(block_table):
-        st = load_library().g2attn_pages_compact(
-            tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, ws.data_ptr(),
-            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_pages_compact")
+    _used_on(stream, src, live, ws)
+    _launch("g2attn_pages_compact", dev, stream, (
+        tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, ws.data_ptr(),
+        ws.numel() * ws.element_size()))
     return src, dst, live
 
 
@@ -973,9 +952,6 @@ def pages_copy(caches, src, dst, *, stream=None):
     if n == 0:
         return
     ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-    with _on(first):
-        st = load_library().g2attn_pages_copy(
-            ptrs, len(caches), sp, dp, n, first.shape[0],
-            first.numel() // first.shape[0] * first.element_size(), _raw_stream(stream, dev))
-    if st != G2ATTN_OK:
-        raise G2AttnError(st, "g2attn_pages_copy")
+    _launch("g2attn_pages_copy", dev, stream, (
+        ptrs, len(caches), sp, dp, n, first.shape[0],
+        first.numel() // first.shape[0] * first.element_size()))

@@ -579,7 +579,7 @@ int launch_rope(g2::RopeParams& P, bool interleaved, cudaStream_t stream) {
     const long long slots = static_cast<long long>(P.tokens) * SL;
     // heads per thread: all the heads' work on one set of sines, but no fewer
     // threads than fill the GPU
-    int hpg = 16;
+    int hpg = g2::ROPE_MAX_HEADS;
     while (hpg > 1 && slots * ((heads + hpg - 1) / hpg) < 148ll * 2048) hpg /= 2;
     P.heads_per_group = hpg;
     P.groups = (heads + hpg - 1) / hpg;

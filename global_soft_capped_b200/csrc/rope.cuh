@@ -26,8 +26,10 @@
 
 namespace g2 {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_UNROLL = 4;  // heads in flight per thread (128 bytes of loads)
+constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_MIN_CTAS = 6;   // 768 threads of up to 85 registers per SM
+constexpr int ROPE_UNROLL = 4;     // heads in flight per thread (128 bytes of loads)
+constexpr int ROPE_MAX_HEADS = 8;  // heads per thread
 
 // What happens to the rotated k (and to v).
 enum RopeMode : int {
@@ -98,8 +100,18 @@ __device__ __forceinline__ int rope_row(const RopeParams& P, int s, int p, int L
     return row;
 }
 
+// Streaming 16-byte load (not .nc: in place, the thread writes it later).
+__device__ __forceinline__ uint4 rope_ld(const __nv_bfloat16* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 template <int D, int MODE, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_MIN_CTAS) rope_kernel(const RopeParams P) {
     constexpr int SL = D / 16;  // slots of a head
     const long long t = static_cast<long long>(blockIdx.x) * ROPE_THREADS + threadIdx.x;
     const int slot = static_cast<int>(t % SL);
@@ -186,8 +198,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) 
                 same[u] = true;
             }
             if (dst[u] == nullptr) continue;
-            a[u] = *reinterpret_cast<const uint4*>(src + e0);
-            b[u] = *reinterpret_cast<const uint4*>(src + e1);
+            a[u] = rope_ld(src + e0);
+            b[u] = rope_ld(src + e1);
         }
 #pragma unroll
         for (int u = 0; u < ROPE_UNROLL; ++u) {
@@ -217,8 +229,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) 
                 b[u] = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
                                   pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
             }
-            *reinterpret_cast<uint4*>(dst[u] + e0) = a[u];
-            *reinterpret_cast<uint4*>(dst[u] + e1) = b[u];
+            __stcs(reinterpret_cast<uint4*>(dst[u] + e0), a[u]);
+            __stcs(reinterpret_cast<uint4*>(dst[u] + e1), b[u]);
         }
     }
 }
