@@ -867,6 +867,13 @@ def pages_workspace(num_seqs, num_blocks, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
+def _pages_ws(workspace, block_table, num_seqs, num_blocks):
+    if workspace is not None:
+        return workspace
+    n = load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
+    return block_table.new_empty((n + 3) // 4)
+
+
 def _table(block_table, ref_counts):
     """(pointer, sequences, columns, pages, counts' pointer) of a page state."""
     if not block_table.is_cuda or block_table.dim() != 2:
@@ -880,11 +887,10 @@ def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, workspace=
                stream=None):
     """Lengthens every sequence by add rows with fresh pages, in place; returns
     granted (num_seqs,) int32, 0 where the pages ran out."""
-    import torch
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    granted = torch.empty(n, dtype=torch.int32, device=dev)
-    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    granted = block_table.new_empty(n)
+    ws = _pages_ws(workspace, block_table, n, nb)
     _used_on(stream, granted, ws)
     _launch("g2attn_pages_grow", dev, stream, (
         tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev), granted.data_ptr(),
@@ -910,8 +916,8 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     table = torch.empty_like(block_table)
-    lens, src, dst, granted = torch.empty((4, n), dtype=torch.int32, device=dev).unbind(0)
-    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    lens, src, dst, granted = block_table.new_empty((4, n)).unbind(0)
+    ws = _pages_ws(workspace, block_table, n, nb)
     _used_on(stream, table, lens, ws)
     _launch("g2attn_pages_fork", dev, stream, (
         tp, _ints("seq_lens", seq_lens, n, dev), _ints("parents", parents, n, dev),
@@ -926,9 +932,9 @@ def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
     import torch
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    src, dst = torch.empty((2, nb // 2), dtype=torch.int32, device=dev).unbind(0)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = pages_workspace(n, nb, dev) if workspace is None else workspace
+    src, dst = block_table.new_empty((2, nb // 2)).unbind(0)
+    live = block_table.new_empty(1)
+    ws = _pages_ws(workspace, block_table, n, nb)
     _used_on(stream, src, live, ws)
     _launch("g2attn_pages_compact", dev, stream, (
         tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, ws.data_ptr(),
@@ -940,18 +946,18 @@ def pages_copy(caches, src, dst, *, stream=None):
     """Copies pages src to pages dst in every cache (num_blocks, ...) of a list
     (K and V of all layers), all of one shape and type."""
     caches = list(caches)
-    if not caches:
-        raise ValueError("caches: expected at least one tensor")
+    if not caches or caches[0].numel() == 0:
+        raise ValueError("caches: expected at least one tensor with pages")
     first = caches[0]
+    dev, shape, kind, n = first.device, first.shape, first.dtype, src.numel()
     for c in caches:
-        if not c.is_cuda or c.device != first.device or c.shape != first.shape \
-                or c.dtype != first.dtype or not c.is_contiguous():
+        if not c.is_cuda or c.device != dev or c.shape != shape or c.dtype != kind \
+                or not c.is_contiguous():
             raise ValueError("caches: expected contiguous CUDA tensors of one shape and type")
-    dev, n = first.device, src.numel()
     sp, dp = _ints("src", src, None, dev), _ints("dst", dst, n, dev)
     if n == 0:
         return
     ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
     _launch("g2attn_pages_copy", dev, stream, (
-        ptrs, len(caches), sp, dp, n, first.shape[0],
-        first.numel() // first.shape[0] * first.element_size()))
+        ptrs, len(caches), sp, dp, n, shape[0],
+        first.numel() // shape[0] * first.element_size()))

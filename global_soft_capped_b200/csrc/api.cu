@@ -1262,7 +1262,7 @@ int g2attn_pages_truncate(int* block_table, int* seq_lens, int* ref_counts, cons
     P.table = block_table;
     P.lens = seq_lens;
     P.arg = keep;
-    g2::pages_truncate_rows<<<num_seqs / 4 + 1, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
+    g2::pages_truncate_rows<<<num_seqs, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
     return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
 }
 

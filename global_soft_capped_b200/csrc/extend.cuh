@@ -902,27 +902,47 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
 
 // Joins the partial results of units that more than one CTA worked on. Where
 // the stretch of CTA blockIdx.x + 1 starts inside a unit, that CTA's record
-// says which partials the unit has; the cuts of a unit share its rows. A warp
-// takes a row (128 columns of it at d = 256): M = max m_i,
+// says which partials the unit has; the cuts of a unit share its rows (at d =
+// 256, halves of rows): M = max m_i,
 //   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
 template <int D, int R>
 __global__ void __launch_bounds__(256) extend_merge(const ExParams P) {
     constexpr int VW = D == 64 ? 2 : 4;           // columns per lane
     constexpr int BLK = D / (32 * VW);            // column blocks of a row
+    constexpr int AHEAD = 4;                      // partials loaded ahead of the weights
     __shared__ float weight[8][EX_MAX_CTAS];
+    __shared__ float part[8][32 * VW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 ra = P.ws_rec[2 * (blockIdx.x + 1)], rb = P.ws_rec[2 * (blockIdx.x + 1) + 1];
     if (ra.x < 0) return;
     const int qrow0 = ra.x, g = ra.y, rows = 2 * ra.z;
     const int c0 = rb.x, parts = rb.y - rb.x + 1, share = rb.z, shares = rb.w;
+    // Few partials: a warp per row. Many (one long sequence): 8 warps share
+    // the partials of a row, so that the loads of all of them are in flight.
+    const int team = parts <= AHEAD ? 1 : (parts <= 2 * AHEAD ? 2 : (parts <= 4 * AHEAD ? 4 : 8));
+    const int member = warp % team, teams = 8 / team;
     float* w = weight[warp];
     // partial i is slot 0 of CTA c0 + i, but for c0's own
     auto slot = [&](int i) -> size_t {
         return static_cast<size_t>(c0 + i) * 2 + (i == 0 ? ra.w : 0);
     };
-    for (int e = share * 8 + warp; e < rows * BLK; e += shares * 8) {
-        const int r = e / BLK, col = (e % BLK) * 32 * VW + lane * VW;
+    auto load = [&](int i, int r, int col, float (&v)[VW]) {
+        const float* o = P.ws_o + (slot(i) * R + r) * D + col;
+        if constexpr (VW == 4)
+            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+        else
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+    };
+    // the whole CTA takes the same number of turns (there is a barrier inside)
+    for (int e0 = share * teams; e0 < rows * BLK; e0 += shares * teams) {
+        const int e = e0 + warp / team;
+        const bool on = e < rows * BLK;
+        const int r = on ? e / BLK : 0, col = (on ? e % BLK : 0) * 32 * VW + lane * VW;
+        float v[AHEAD][VW];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (member + k * team < parts) load(member + k * team, r, col, v[k]);
         float M = -INFINITY;
         for (int i = lane; i < parts; i += 32) {
             w[i] = P.ws_s[(slot(i) * R + r) * 4];
@@ -946,18 +966,35 @@ __global__ void __launch_bounds__(256) extend_merge(const ExParams P) {
         float acc[VW];
 #pragma unroll
         for (int k = 0; k < VW; ++k) acc[k] = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) {
-            const float* o = P.ws_o + (slot(i) * R + r) * D + col;
-            float v[VW];
-            if constexpr (VW == 4)
-                *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-            else
-                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
 #pragma unroll
-            for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[i], v[k], acc[k]);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (member + k * team < parts) {
+#pragma unroll
+                for (int c = 0; c < VW; ++c) acc[c] = fmaf(w[member + k * team], v[k][c], acc[c]);
+            }
         }
-        __syncwarp();  // w is written anew for the next row
+#pragma unroll 4
+        for (int i = member + AHEAD * team; i < parts; i += team) {
+            float u[VW];
+            load(i, r, col, u);
+#pragma unroll
+            for (int c = 0; c < VW; ++c) acc[c] = fmaf(w[i], u[c], acc[c]);
+        }
+        if (team > 1) {  // in the order of the members
+#pragma unroll
+            for (int c = 0; c < VW; ++c) part[warp][c * 32 + lane] = acc[c];
+            __syncthreads();
+            if (member == 0) {
+                for (int k = 1; k < team; ++k) {
+#pragma unroll
+                    for (int c = 0; c < VW; ++c) acc[c] += part[warp + k][c * 32 + lane];
+                }
+            }
+            __syncthreads();
+        } else {
+            __syncwarp();  // w is written anew for the next row
+        }
+        if (!on || member != 0) continue;
         const float inv = l > 0.f ? 1.0f / l : 0.f;
         const int qrow = qrow0 + (r >> 1), h = 2 * g + (r & 1);
         uint32_t* dst = reinterpret_cast<uint32_t*>(

@@ -20,6 +20,7 @@ namespace g2 {
 constexpr int PG_THREADS = 1024;
 constexpr int PG_PER = 16;                       // pages per thread and scan step
 constexpr int PG_STEP = PG_THREADS * PG_PER;
+constexpr int PG_BASES = 2048;                   // sequences whose ranks stay in shared memory
 constexpr int PG_MAX_CACHES = 128;               // cache pointers per copy launch
 constexpr int PG_COPY_THREADS = 256;
 constexpr int PG_COPY_UNROLL = 8;                // 16-byte vectors in flight per thread
@@ -36,7 +37,7 @@ struct PagesParams {
     int* src;              // fork, compact: pages to copy (-1: none)
     int* dst;
     int* num_live;         // compact
-    int* ws_base;          // [num_seqs] rank of a sequence's first fresh page
+    int* ws_base;          // [num_seqs] rank of a sequence's first fresh page (past PG_BASES)
     int* ws_pages;         // [num_blocks] fresh pages by rank; compact: new page of a moved one
     int num_seqs, num_blocks, block_shift, max_blocks;
 };
@@ -94,8 +95,8 @@ __device__ __forceinline__ unsigned int pg_bits(const int* refs, int n, long lon
     return m;
 }
 
-__device__ __forceinline__ int pg_pages(long long rows, int shift) {
-    return static_cast<int>((rows + (1ll << shift) - 1) >> shift);
+__device__ __forceinline__ long long pg_pages(long long rows, int shift) {
+    return (rows + (1ll << shift) - 1) >> shift;
 }
 
 __device__ __forceinline__ int pg_len(const PagesParams& P, const int* lens, int s) {
@@ -114,21 +115,22 @@ __device__ __forceinline__ int pg_need(const PagesParams& P, int s, bool& fits) 
         return (pg_len(P, P.lens_in, p) & ((1 << P.block_shift) - 1)) != 0;
     } else {
         const long long old = pg_len(P, P.lens, s);
-        const int have = pg_pages(old, P.block_shift);
-        const int want = pg_pages(old + max(0, P.arg[s]), P.block_shift);
+        const long long have = pg_pages(old, P.block_shift);
+        const long long want = pg_pages(old + max(0, P.arg[s]), P.block_shift);
         fits = want <= P.max_blocks;
-        return fits ? want - have : 0;
+        return fits ? static_cast<int>(want - have) : 0;
     }
 }
 
 // One CTA: ranks the requests, finds the free pages of lowest index and grants
 // every request that its rank leaves room for. Grow: writes the new entries,
-// counts and lengths. Fork: leaves the fresh page of each sequence in ws_base
-// (-1: none).
+// counts and lengths. Fork: leaves the fresh page of each sequence in dst (-1:
+// none).
 template <bool FORK>
 __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) {
     __shared__ int red[33];
     __shared__ long long red64[33];
+    __shared__ int base[PG_BASES];
     const int tid = threadIdx.x;
     long long wanted = 0;  // requests can exceed 32 bits in sum
     for (int b = 0; b < P.num_seqs; b += PG_THREADS) {
@@ -138,7 +140,10 @@ __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) 
         long long total;
         const long long r = wanted + pg_scan(need, red64, total);
         // a rank that no cache has is refused below, whatever it is exactly
-        if (s < P.num_seqs) P.ws_base[s] = static_cast<int>(min(r, 0x7fffffffll));
+        if (s < P.num_seqs) {
+            const int first = static_cast<int>(min(r, 0x7fffffffll));
+            if (s < PG_BASES) base[s] = first; else P.ws_base[s] = first;
+        }
         wanted += total;
     }
     int found = 0;
@@ -154,26 +159,39 @@ __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) 
         found += total;
     }
     __syncthreads();  // ws_base and ws_pages, written by this CTA, are read below
-    const int lane = tid & 31;
-    for (int s = tid >> 5; s < P.num_seqs; s += PG_THREADS / 32) {
+    // one thread per fresh page: its sequence is the last one whose rank is not
+    // above the page's (of equal ranks the last asks for pages, the others do not)
+    const int given = static_cast<int>(min(static_cast<long long>(found), wanted));
+    for (int r = tid; r < given; r += PG_THREADS) {
+        int lo = 0, hi = P.num_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((mid < PG_BASES ? base[mid] : P.ws_base[mid]) <= r) lo = mid; else hi = mid - 1;
+        }
+        const int first = lo < PG_BASES ? base[lo] : P.ws_base[lo];
+        bool fits;
+        const int need = pg_need<FORK>(P, lo, fits);
+        if (static_cast<long long>(first) + need > found) continue;  // refused
+        const int page = P.ws_pages[r];
+        if constexpr (FORK) {
+            P.dst[lo] = page;
+        } else {
+            const long long have = pg_pages(pg_len(P, P.lens, lo), P.block_shift);
+            P.table[static_cast<size_t>(lo) * P.max_blocks + have + (r - first)] = page;
+            P.refs[page] = 1;
+        }
+    }
+    __syncthreads();  // the lengths are overwritten only now
+    for (int s = tid; s < P.num_seqs; s += PG_THREADS) {
         bool fits;
         const int need = pg_need<FORK>(P, s, fits);
-        const int base = P.ws_base[s];
-        const bool ok = fits && (need == 0 || static_cast<long long>(base) + need <= found);
-        if (lane == 0) P.granted[s] = ok;
-        __syncwarp();  // every lane has read the request before it is overwritten
+        const int first = s < PG_BASES ? base[s] : P.ws_base[s];
+        const bool ok = fits && (need == 0 || static_cast<long long>(first) + need <= found);
+        P.granted[s] = ok;
         if constexpr (FORK) {
-            if (lane == 0) P.ws_base[s] = ok && need != 0 ? P.ws_pages[base] : -1;
+            if (!ok || need == 0) P.dst[s] = -1;
         } else if (ok) {
-            const int old = pg_len(P, P.lens, s);
-            const int have = pg_pages(old, P.block_shift);
-            for (int c = lane; c < need; c += 32) {
-                const int page = P.ws_pages[base + c];
-                P.table[static_cast<size_t>(s) * P.max_blocks + have + c] = page;
-                P.refs[page] = 1;
-            }
-            __syncwarp();
-            if (lane == 0) P.lens[s] = old + max(0, P.arg[s]);
+            P.lens[s] = pg_len(P, P.lens, s) + max(0, P.arg[s]);
         }
     }
 }
@@ -189,14 +207,14 @@ __global__ void __launch_bounds__(128) pages_fork_rows(const PagesParams P) {
         for (int c = threadIdx.x; c < P.max_blocks; c += blockDim.x) out[c] = own[c];
         if (threadIdx.x == 0) {
             P.lens[s] = P.lens_in[s];
-            P.src[s] = P.dst[s] = -1;
+            P.src[s] = -1;  // dst already is
         }
         return;
     }
     const int* from = P.table_in + static_cast<size_t>(p) * P.max_blocks;
     const int L = pg_len(P, P.lens_in, p);
     const int full = L >> P.block_shift;
-    const int fresh = P.ws_base[s];
+    const int fresh = P.dst[s];
     for (int c = threadIdx.x; c < P.max_blocks; c += blockDim.x) {
         const int had = own[c];
         const int gets = c < full ? from[c] : (c == full ? fresh : -1);
@@ -207,25 +225,27 @@ __global__ void __launch_bounds__(128) pages_fork_rows(const PagesParams P) {
     if (threadIdx.x == 0) {
         P.lens[s] = L;
         P.src[s] = fresh >= 0 ? from[full] : -1;
-        P.dst[s] = fresh;
     }
 }
 
-// One warp per sequence: pages behind the kept rows go back.
+// One CTA per sequence: pages behind the kept rows go back.
 __global__ void __launch_bounds__(128) pages_truncate_rows(const PagesParams P) {
-    const int s = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (s >= P.num_seqs) return;
-    const int lane = threadIdx.x & 31;
+    const int s = blockIdx.x;
     const int keep = min(pg_len(P, P.lens, s), max(0, P.arg[s]));
-    __syncwarp();
-    for (int c = pg_pages(keep, P.block_shift) + lane; c < P.max_blocks; c += 32) {
-        int* e = P.table + static_cast<size_t>(s) * P.max_blocks + c;
-        const int page = *e;
-        if (page < 0) continue;
-        if (page < P.num_blocks) atomicSub(P.refs + page, 1);
-        *e = -1;
+    int* row = P.table + static_cast<size_t>(s) * P.max_blocks;
+    for (long long c = pg_pages(keep, P.block_shift) + threadIdx.x; c < P.max_blocks; c += 4 * 128) {
+        int page[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) page[u] = c + 128 * u < P.max_blocks ? row[c + 128 * u] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (page[u] < 0) continue;
+            if (page[u] < P.num_blocks) atomicSub(P.refs + page[u], 1);
+            row[c + 128 * u] = -1;
+        }
     }
-    if (lane == 0) P.lens[s] = keep;
+    __syncthreads();  // every thread has read the old length
+    if (threadIdx.x == 0) P.lens[s] = keep;
 }
 
 // One CTA: counts the live pages, then pairs the i-th live page at or above

@@ -223,6 +223,14 @@ def test_huge_requests_sum_past_32_bits():
     assert int((table >= 0).sum()) == 5
 
 
+def test_lengths_past_32_bits_are_refused():
+    """Pages of one row: the length asked for does not fit 32 bits."""
+    p = Pair(2, 40, 100, 1)
+    assert p.grow([30, 0]).tolist() == [1, 1]
+    assert p.grow([2 ** 31 - 1, 2 ** 31 - 1]).tolist() == [0, 0]
+    assert p.grow([10, 40]).tolist() == [1, 1]
+
+
 def test_forks_of_one_parent_and_swaps():
     p = Pair(6, 4, 40, 8)
     p.grow([20, 16, 0, 5, 1, 0])
