@@ -75,6 +75,9 @@ struct ExCfg {
     static constexpr int Q_BYTES = R * D * 2;
     static constexpr int QB = R * D <= 8192 ? 2 : 1;      // Q buffers
     static constexpr int P_BYTES = R * EX_BN * 2;         // two buffers
+    // P with its rows contiguous (R = 64: a key's 64 rows are one 128-byte
+    // line, which a thread writes 16 bytes at a time) or its keys (R < 64)
+    static constexpr bool P_ROWS = R == 64;
     static constexpr int FIXED = QB * Q_BYTES + 2 * P_BYTES;
     // rows 64..127 of the d = 64 product read one chunk past their slot: the
     // tiles after the ring must span that
@@ -202,10 +205,17 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const long long* cum,
     int qb, T;
     pf_seq_rows(P.cu_q, lo, P.total_q, &qb, &T);
     const int L = ex_len(P, lo);
-    const long long per_g = (cum[lo + 1] - cum[lo]) / P.Hkv;
+    const long long n = cum[lo + 1] - cum[lo];
     long long rem = x - cum[lo];
-    U.g = static_cast<int>(rem / per_g);
-    rem -= U.g * per_g;
+    if (n <= 0x7fffffffll) {  // (64-bit divisions take hundreds of cycles)
+        const unsigned int per_g = static_cast<unsigned int>(n) / static_cast<unsigned int>(P.Hkv);
+        U.g = static_cast<int>(static_cast<unsigned int>(rem) / per_g);
+        rem -= static_cast<long long>(U.g) * per_g;
+    } else {
+        const long long per_g = n / P.Hkv;
+        U.g = static_cast<int>(rem / per_g);
+        rem -= U.g * per_g;
+    }
     for (U.t0 = 0;; U.t0 += TQ) {
         U.tvalid = min(TQ, T - U.t0);
         U.p0 = L - T + U.t0;
@@ -355,24 +365,6 @@ __device__ __forceinline__ void ex_scores(const ExParams& P, uint32_t addr, floa
     }
 }
 
-// p += the negated references of the HC rows; returns the largest result.
-template <int HC>
-__device__ __forceinline__ float ex_less_ref(const float* neg, float (&p)[HC]) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < HC; c += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(neg + c);
-        const float2 a = add2(make_float2(p[c], p[c + 1]), make_float2(f.x, f.y));
-        const float2 b = add2(make_float2(p[c + 2], p[c + 3]), make_float2(f.z, f.w));
-        p[c] = a.x;
-        p[c + 1] = a.y;
-        p[c + 2] = b.x;
-        p[c + 3] = b.y;
-        top = fmax3f(top, fmaxf(a.x, a.y), fmaxf(b.x, b.y));
-    }
-    return top;
-}
-
 // SM = PF_SM_FIXED or PF_SM_CAP (any running max; has_cap tells the cap).
 template <int D, int R, int SM>
 __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const ExParams P) {
@@ -400,7 +392,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
     uint64_t* wg_sum = bars + 30;          // [4]
     uint64_t* wg_vote = bars + 34;         // [4]
     // votes of the warps of a warpgroup, a byte each [tile parity][warpgroup]
-    volatile uint32_t* votes = reinterpret_cast<volatile uint32_t*>(bars + 40);
+    volatile unsigned char* votes = reinterpret_cast<volatile unsigned char*>(bars + 40);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 44);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 45);
     // row statistics that they exchange: maxima [exchange parity][warpgroup]
@@ -569,7 +561,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         // ------------------------------------------------------ UMMA issuer
         if (lane == 0 && x0 < x1) {
             constexpr uint32_t IDESC_S = idesc_bf16(128, R, false);
-            constexpr uint32_t IDESC_O = idesc_bf16(128, R, false) | (1u << 15);  // A MN-major
+            constexpr uint32_t IDESC_O = idesc_bf16(128, R, C::P_ROWS) | (1u << 15);  // A MN-major
             constexpr uint32_t HI = sdesc_hi(1024);
             const uint32_t k_lo0 = sdesc_lo(smem_u32(sSlots), 16);
             const uint32_t v_lo0 = sdesc_lo(smem_u32(sSlots), C::CH_BYTES);  // 64-column chunks
@@ -635,8 +627,9 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
 #pragma unroll
                         for (int kk = 0; kk < EX_BN / 16; ++kk)
                             umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4),
-                                       p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2, HI,
-                                       IDESC_O, !(first_v && kk == 0));
+                                       C::P_ROWS ? p_lo + kk * ((16 * 128) >> 4)
+                                                 : p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
+                                       HI, IDESC_O, !(first_v && kk == 0));
                         umma_commit(&slot_empty[slot]);
                     }
                     if (!ok) break;
@@ -657,18 +650,26 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
         const uint32_t s_addr = tmem + lane_addr + wg * HC;
         const uint32_t o_addr = tmem + lane_addr + 2 * R + wg * HC;
-        // P: row r, this thread's pair of keys (even, odd): one 32-bit word.
-        // Even lanes store rows c8 + 0..3, odd lanes rows c8 + 4..7; a row's
-        // swizzle depends on r mod 8 only, so four addresses serve every c8.
+        // P, keys contiguous: row r, this thread's pair of keys (even, odd) is
+        // one 32-bit word. Even lanes store rows c8 + 0..3, odd lanes rows c8 +
+        // 4..7; a row's swizzle depends on r mod 8 only, so four addresses
+        // serve every c8. Rows contiguous: the key's line, this warpgroup's
+        // 16-byte pieces of it.
         const bool odd = lane & 1;
         const uint32_t p_sel = odd ? 0x3276u : 0x5410u;  // (got, own) high or (own, got) low halves
         uint32_t p_addr[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int r8 = k + (odd ? 4 : 0);
-            p_addr[k] = (smem_u32(sP) + (key_l >> 6) * (R * 128) + (wg * HC + r8) * 128 +
-                         (key_l & 62) * 2) ^ (r8 << 4);
+            p_addr[k] = C::P_ROWS
+                ? smem_u32(sP) + key_l * 128 + (((wg * HC / 8 + k) ^ (key_l & 7)) << 4)
+                : (smem_u32(sP) + (key_l >> 6) * (R * 128) + (wg * HC + r8) * 128 +
+                   (key_l & 62) * 2) ^ (r8 << 4);
         }
+        // rows of pair c: c and c + 4 of every eight (keys contiguous), or 2c and 2c + 1
+        auto pair_row = [](int c, int second) -> int {
+            return C::P_ROWS ? 2 * c + second : (c >> 2) * 8 + (c & 3) + 4 * second;
+        };
         bool ok = true;
         uint32_t unit = 0, raises = 0, refs = 0;
         float* neg = nullptr;  // this warpgroup's negated references
@@ -679,8 +680,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             const long long end = U.first + U.tiles;
             const int t_begin = static_cast<int>(x - U.first);
             const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
-            // sums of the weights of rows c and c + 4 of every eight: fp32 ones,
-            // and the rounded ones
+            // sums of the weights of pairs of rows (see pair_row), fp32 ones and
+            // the rounded ones
             float2 l32[HC / 2], lr[HC / 2];
 #pragma unroll
             for (int c = 0; c < HC / 2; ++c) l32[c] = lr[c] = make_float2(0.f, 0.f);
@@ -689,48 +690,61 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 if (lane < HC) neg[lane] = -EX_NO_MAX;  // all four warps write the same
                 __syncwarp();
             }
-            for (int t = t_begin; t < t_end; ++t) {
-                const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
+            // Scores of tile t in log2 units (less the fixed shift), masked. With
+            // a running reference, also this warp's vote on raising it.
+            float next[HC];
+            auto peek = [&](int t, uint32_t it) -> bool {
                 const uint32_t b = it & 1;
-                ok = mbar_wait(&s_full[b], (it >> 1) & 1, abort_flag, lim, SITE_EX_SM);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                bool k = mbar_wait(&s_full[b], (it >> 1) & 1, abort_flag, lim, SITE_EX_SM);
+                k = __all_sync(0xffffffffu, k);
+                if (!k) return false;
                 tc_fence_after();
-                float p[HC];
-                ex_scores<HC, FIX>(P, s_addr + b * R, p);
+                ex_scores<HC, FIX>(P, s_addr + b * R, next);
                 const int k0 = U.lo + t * EX_BN;
-                const int key = k0 + key_l;
                 // an inner tile is seen whole by every row
-                const bool edge = k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
-                                  (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window);
-                auto mask = [&]() {
+                if (k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
+                    (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window)) {
+                    const int key = k0 + key_l;
 #pragma unroll
                     for (int c = 0; c < HC; ++c) {
                         const int pos = U.p0 + ((wg * HC + c) >> 1);
                         if (key > pos || key >= U.hi || (P.window > 0 && pos - key >= P.window))
-                            p[c] = -INFINITY;
+                            next[c] = -INFINITY;
                     }
-                };
-                if (edge) mask();
+                }
                 if constexpr (!FIX) {
-                    const float top = ex_less_ref<HC>(neg, p);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < HC; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(neg + c);
+                        const float2 u = add2(make_float2(next[c], next[c + 1]), make_float2(f.x, f.y));
+                        const float2 v =
+                            add2(make_float2(next[c + 2], next[c + 3]), make_float2(f.z, f.w));
+                        top = fmax3f(top, fmaxf(u.x, u.y), fmaxf(v.x, v.y));
+                    }
                     const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
-                    volatile uint32_t* vote = votes + (b * C::NWG + wg);
                     if (lane == 0) {
-                        reinterpret_cast<volatile unsigned char*>(vote)[qd] = raise;
+                        votes[(b * C::NWG + wg) * 4 + qd] = raise;
                         mbar_arrive(&wg_vote[wg]);
                     }
+                }
+                return true;
+            };
+            ok = peek(t_begin, static_cast<uint32_t>(x - x0));
+            for (int t = t_begin; t < t_end && ok; ++t) {
+                const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
+                const uint32_t b = it & 1;
+                if constexpr (!FIX) {
                     ok = mbar_wait(&wg_vote[wg], it & 1, abort_flag, lim, SITE_EX_SM);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (*vote != 0) {  // the same decision in the whole warpgroup
+                    // the same decision in the whole warpgroup
+                    if (*reinterpret_cast<volatile uint32_t*>(votes + (b * C::NWG + wg) * 4) != 0) {
                         float* st = s_max + ((raises & 1) * C::NWG + wg) * 4 * HC;
-                        ex_scores<HC, FIX>(P, s_addr + b * R, p);
-                        if (edge) mask();
                         {
                             float mx[HC];
 #pragma unroll
-                            for (int c = 0; c < HC; ++c) mx[c] = p[c];
+                            for (int c = 0; c < HC; ++c) mx[c] = next[c];
                             const float w = ex_reduce<HC, true>(mx);
                             if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
                         }
@@ -742,25 +756,25 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         // new references into the other buffer (the other warps
                         // may still read this one), and the factors of what was
                         // summed so far (0 where nothing was)
-                        float* next = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
+                        float* to = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
                         float* fac = s_fac + warp * HC;
                         if (lane < HC) {
                             const float m = -neg[lane];
                             const float n = fmaxf(fmaxf(m, st[lane]),
                                                   fmax3f(st[HC + lane], st[2 * HC + lane],
                                                          st[3 * HC + lane]));
-                            next[lane] = -n;
+                            to[lane] = -n;
                             fac[lane] = ex2_approx(m - n);
                         }
-                        neg = next;
+                        neg = to;
                         __syncwarp();
 #pragma unroll
                         for (int c = 0; c < HC / 2; ++c) {
-                            const int r = (c >> 2) * 8 + (c & 3);
-                            l32[c].x *= fac[r];
-                            l32[c].y *= fac[r + 4];
-                            lr[c].x *= fac[r];
-                            lr[c].y *= fac[r + 4];
+                            const float fx = fac[pair_row(c, 0)], fy = fac[pair_row(c, 1)];
+                            l32[c].x *= fx;
+                            l32[c].y *= fy;
+                            lr[c].x *= fx;
+                            lr[c].y *= fy;
                         }
                         if (t > t_begin) {  // O must hold every tile before this
                             const uint32_t pv = it - 1;
@@ -783,33 +797,63 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                             tmem_wait_st();
                         }
                         __syncwarp();  // fac is read before the next raise writes it
-                        ex_less_ref<HC>(neg, p);
                     }
+                }
+                float p[HC];
+#pragma unroll
+                for (int c = 0; c < HC; c += 4) {
+                    if constexpr (FIX) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) p[c + k] = next[c + k];
+                    } else {
+                        const float4 f = *reinterpret_cast<const float4*>(neg + c);
+                        const float2 u = add2(make_float2(next[c], next[c + 1]), make_float2(f.x, f.y));
+                        const float2 v =
+                            add2(make_float2(next[c + 2], next[c + 3]), make_float2(f.z, f.w));
+                        p[c] = u.x;
+                        p[c + 1] = u.y;
+                        p[c + 2] = v.x;
+                        p[c + 3] = v.y;
+                    }
+                }
+                // the next tile's scores (and vote) while this one's weights go out
+                if (t + 1 < t_end) {
+                    ok = peek(t + 1, it + 1);
+                    if (!ok) break;
                 }
 #pragma unroll
                 for (int c = 0; c < HC; ++c) p[c] = ex2_approx(p[c]);
-                if (it >= 2) {  // P buffer: the product of tile it - 2 has read it
-                    ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                }
-                // rows c and c + 4: lanes 2j, 2j+1 swap halves and store the key
-                // pair of one row each (a warp's store hits every bank once)
+                // The P buffer is free: S of this tile was issued after the
+                // product of tile it - 2, and its completion counts that in.
                 const uint32_t p_buf = b * C::P_BYTES;
 #pragma unroll
                 for (int c8 = 0; c8 < HC; c8 += 8) {
+                    uint32_t line[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int c = c8 + k, i = c8 / 2 + k;
-                        const uint32_t own = pack_bf16x2(p[c], p[c + 4]);
-                        l32[i] = add2(l32[i], make_float2(p[c], p[c + 4]));
+                        // the pair of rows that share a word or an exchange
+                        const int c = c8 + (C::P_ROWS ? 2 * k : k), d = C::P_ROWS ? 1 : 4;
+                        const int i = c8 / 2 + k;
+                        const uint32_t own = pack_bf16x2(p[c], p[c + d]);
+                        l32[i] = add2(l32[i], make_float2(p[c], p[c + d]));
                         lr[i] = add_bf16x2_f32(lr[i], own);
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
-                        const uint32_t w = __byte_perm(own, got, p_sel);
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_addr[k] + p_buf + c8 * 128),
-                                     "r"(w)
-                                     : "memory");
+                        if constexpr (C::P_ROWS) {
+                            line[k] = own;
+                        } else {
+                            // lanes 2j, 2j+1 swap halves and store the key pair of
+                            // one row each (a warp's store hits every bank once)
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(
+                                             p_addr[k] + p_buf + c8 * 128),
+                                         "r"(__byte_perm(own, got, p_sel))
+                                         : "memory");
+                        }
                     }
+                    if constexpr (C::P_ROWS)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         p_addr[c8 / 8] + p_buf),
+                                     "r"(line[0]), "r"(line[1]), "r"(line[2]), "r"(line[3])
+                                     : "memory");
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -823,8 +867,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 auto spread = [&](const float2 (&l)[HC / 2]) {
 #pragma unroll
                     for (int c = 0; c < HC / 2; ++c) {
-                        v[(c >> 2) * 8 + (c & 3)] = l[c].x;
-                        v[(c >> 2) * 8 + (c & 3) + 4] = l[c].y;
+                        v[pair_row(c, 0)] = l[c].x;
+                        v[pair_row(c, 1)] = l[c].y;
                     }
                 };
                 spread(l32);
@@ -840,6 +884,14 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
             }
+            float inv[HC];
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+                float l = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) l += ssum[(w * HC + c) * 2 + 1];
+                inv[c] = l > 0.f ? rcp_approx(l) : 0.f;
+            }
             ok = mbar_wait(o_full, unit & 1, abort_flag, lim, SITE_EX_SM);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -848,6 +900,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             // a stretch's first segment has slot 0, its last one slot 1
             const size_t ws = static_cast<size_t>(blockIdx.x) * 2 + (unit == 0 ? 0 : 1);
             const int rows = 2 * U.tvalid;
+            __nv_bfloat16* out0 = P.out + (static_cast<size_t>(U.qrow) * P.H + 2 * U.g) * D;
 #pragma unroll
             for (int o = 0; o < C::O_BLOCKS; ++o) {
                 float a[HC];
@@ -858,16 +911,11 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 for (int c = 0; c < HC; ++c) {
                     const int r = wg * HC + c;
                     if (r >= rows) continue;
-                    if (whole) {
-                        float l = 0.f;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) l += ssum[(w * HC + c) * 2 + 1];
-                        const float v = l > 0.f ? a[c] / l : 0.f;
-                        P.out[(static_cast<size_t>(U.qrow + (r >> 1)) * P.H + 2 * U.g + (r & 1)) * D +
-                              dcol] = __float2bfloat16_rn(v);
-                    } else {
+                    if (whole)
+                        out0[(static_cast<size_t>(r >> 1) * P.H + (r & 1)) * D + dcol] =
+                            __float2bfloat16_rn(a[c] * inv[c]);
+                    else
                         P.ws_o[(ws * R + r) * D + dcol] = a[c];
-                    }
                 }
             }
             if (key_l < HC && wg * HC + key_l < rows) {
