@@ -52,8 +52,14 @@ namespace g2 {
 
 constexpr int EX_BN = 128;            // keys per tile
 constexpr int EX_PROD_WARPS = 2;
+constexpr int EX_S_BUFS = 3;          // S tiles in tensor memory
+constexpr int EX_LAG = EX_S_BUFS - 1; // tiles by which V and its product follow K and S
+constexpr int EX_MAX_SLOTS = 12;      // ring slots, whatever fits
 constexpr int EX_MAX_SEQS = 1024;     // per-launch table in shared memory
 constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
+// Tiles a launch numbers at most (2^38 keys over all heads: days of work; the
+// queries of tiles past it are not answered).
+constexpr long long EX_MAX_TILES = 0x7fffffffll;
 constexpr float EX_RAISE_LOG2 = 64.0f;   // see the softmax above
 constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key yet
 
@@ -73,26 +79,33 @@ struct ExCfg {
     static constexpr int NCH = SLOT_COLS / 64;            // 64-column chunks per slot
     static constexpr int CH_BYTES = EX_BN * 128;          // 16 KB
     static constexpr int Q_BYTES = R * D * 2;
-    static constexpr int QB = R * D <= 8192 ? 2 : 1;      // Q buffers
-    static constexpr int P_BYTES = R * EX_BN * 2;         // two buffers
+    static constexpr int QB = R == 64 ? 1 : 2;            // Q buffers (R = 64: more ring slots)
+    static constexpr int P_BYTES = R * EX_BN * 2;
     // P with its rows contiguous (R = 64: a key's 64 rows are one 128-byte
     // line, which a thread writes 16 bytes at a time) or its keys (R < 64)
     static constexpr bool P_ROWS = R == 64;
+    // R = 64: the sums of the rounded weights come from the tensor core, as one
+    // more block of O^T whose "V" is all ones, 8 columns of tensor memory (16
+    // registers and a fifth of the weights' instructions less per thread)
+    static constexpr int ONES = R == 64 ? 1 : 0;
     static constexpr int FIXED = QB * Q_BYTES + 2 * P_BYTES;
     // rows 64..127 of the d = 64 product read one chunk past their slot: the
     // tiles after the ring must span that
     static constexpr int PAD = D == 64 && FIXED < CH_BYTES ? CH_BYTES - FIXED : 0;
-    static constexpr int CUM_BYTES = 8 * (EX_MAX_SEQS + 1);
-    static constexpr int CTRL_BYTES = 448 + 30 * R * 4;
+    static constexpr int CUM_BYTES = 4 * (EX_MAX_SEQS + 1);
+    static constexpr int CTRL_BYTES = 512 + (8 + (ONES ? 8 : 16) + 6) * R * 4;
     static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - PAD - CUM_BYTES - CTRL_BYTES - 64;
     static constexpr int NS_FIT = BUDGET / SLOT_BYTES;
-    static constexpr int NS = NS_FIT > 8 ? 8 : NS_FIT;
+    static constexpr int NS = NS_FIT > EX_MAX_SLOTS ? EX_MAX_SLOTS : NS_FIT;
     static constexpr int SMEM_BYTES =
         1024 + NS * SLOT_BYTES + FIXED + PAD + CUM_BYTES + CTRL_BYTES + 64;
     static constexpr int O_BLOCKS = D <= 128 ? 1 : D / 128;  // M = 128 blocks of O^T
-    static constexpr int TMEM_USED = 2 * R + O_BLOCKS * R;
-    static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : (TMEM_USED <= 128 ? 128 : 256);
-    static_assert(NS >= 2 * KSL && SMEM_BYTES <= 227 * 1024 && TMEM_USED <= 256, "budget");
+    static constexpr int O_COL = EX_S_BUFS * R;
+    static constexpr int ONES_COL = O_COL + (O_BLOCKS + ONES) * R;
+    static constexpr int TMEM_USED = ONES_COL + 8 * ONES;
+    static constexpr int TMEM_COLS =
+        TMEM_USED <= 64 ? 64 : (TMEM_USED <= 128 ? 128 : (TMEM_USED <= 256 ? 256 : 512));
+    static_assert(NS >= 2 * KSL && SMEM_BYTES <= 227 * 1024 && TMEM_USED <= 512, "budget");
 };
 
 struct ExParams {
@@ -156,8 +169,9 @@ __device__ __forceinline__ long long ex_seq_tiles(const ExParams& P, int s) {
 
 // cum[s] = tiles before sequence s, cum[num_seqs] = all. Whole CTA.
 template <int TQ>
-__device__ __forceinline__ void ex_cum(const ExParams& P, long long* cum) {
-    for (int s = threadIdx.x; s < P.num_seqs; s += blockDim.x) cum[s + 1] = ex_seq_tiles<TQ>(P, s);
+__device__ __forceinline__ void ex_cum(const ExParams& P, unsigned int* cum) {
+    for (int s = threadIdx.x; s < P.num_seqs; s += blockDim.x)
+        cum[s + 1] = static_cast<unsigned int>(min(ex_seq_tiles<TQ>(P, s), EX_MAX_TILES));
     if (threadIdx.x == 0) cum[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -170,8 +184,8 @@ __device__ __forceinline__ void ex_cum(const ExParams& P, long long* cum) {
                 const long long y = __shfl_up_sync(0xffffffffu, x, o);
                 if (static_cast<int>(threadIdx.x) >= o) x += y;
             }
-            x += base;
-            if (i <= P.num_seqs) cum[i] = x;
+            x = min(x + base, EX_MAX_TILES);
+            if (i <= P.num_seqs) cum[i] = static_cast<unsigned int>(x);
             base = __shfl_sync(0xffffffffu, x, 31);
         }
     }
@@ -194,7 +208,7 @@ __device__ __forceinline__ long long ex_owner(long long tile, long long all, lon
 
 // The unit that holds tile `x` of the line.
 template <int TQ>
-__device__ __forceinline__ void ex_unit(const ExParams& P, const long long* cum, long long x,
+__device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* cum, long long x,
                                         ExUnit& U) {
     int lo = 0, hi = P.num_seqs - 1;  // last s with cum[s] <= x
     while (lo < hi) {
@@ -205,24 +219,18 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const long long* cum,
     int qb, T;
     pf_seq_rows(P.cu_q, lo, P.total_q, &qb, &T);
     const int L = ex_len(P, lo);
-    const long long n = cum[lo + 1] - cum[lo];
-    long long rem = x - cum[lo];
-    if (n <= 0x7fffffffll) {  // (64-bit divisions take hundreds of cycles)
-        const unsigned int per_g = static_cast<unsigned int>(n) / static_cast<unsigned int>(P.Hkv);
-        U.g = static_cast<int>(static_cast<unsigned int>(rem) / per_g);
-        rem -= static_cast<long long>(U.g) * per_g;
-    } else {
-        const long long per_g = n / P.Hkv;
-        U.g = static_cast<int>(rem / per_g);
-        rem -= U.g * per_g;
-    }
+    const unsigned int n = cum[lo + 1] - cum[lo], at = static_cast<unsigned int>(x) - cum[lo];
+    const unsigned int per_g = max(1u, n / static_cast<unsigned int>(P.Hkv));
+    U.g = static_cast<int>(min(at / per_g, static_cast<unsigned int>(P.Hkv) - 1));
+    unsigned int rem = at - U.g * per_g;
     for (U.t0 = 0;; U.t0 += TQ) {
         U.tvalid = min(TQ, T - U.t0);
         U.p0 = L - T + U.t0;
         U.tiles = ex_range(U.p0, U.tvalid, L, P.window, U.lo, U.hi);
-        if (rem < U.tiles || U.t0 + TQ >= T) break;
+        if (rem < static_cast<unsigned int>(U.tiles) || U.t0 + TQ >= T) break;
         rem -= U.tiles;
     }
+    rem = min(rem, static_cast<unsigned int>(U.tiles) - 1);
     U.first = x - rem;
     U.qrow = qb + U.t0;
 }
@@ -378,28 +386,28 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
     unsigned char* sQ = sSlots + C::NS * C::SLOT_BYTES;
     unsigned char* sP = sQ + C::QB * C::Q_BYTES;
     unsigned char* ctrl = sP + 2 * C::P_BYTES + C::PAD;
-    long long* cum = reinterpret_cast<long long*>(ctrl);
+    unsigned int* cum = reinterpret_cast<unsigned int*>(ctrl);
     uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl + ((C::CUM_BYTES + 63) / 64) * 64);
-    uint64_t* slot_full = bars;            // [8]
-    uint64_t* slot_empty = bars + 8;       // [8]
-    uint64_t* q_empty = bars + 16;         // [2]
-    uint64_t* s_full = bars + 18;          // [2]
-    uint64_t* p_full = bars + 20;          // [2]
-    uint64_t* p_empty = bars + 22;         // [2]
-    uint64_t* o_full = bars + 24;
-    uint64_t* drain = bars + 25;
-    uint64_t* wg_max = bars + 26;          // [4] warpgroup exchanges
-    uint64_t* wg_sum = bars + 30;          // [4]
-    uint64_t* wg_vote = bars + 34;         // [4]
+    uint64_t* slot_full = bars;                       // [EX_MAX_SLOTS]
+    uint64_t* slot_empty = bars + EX_MAX_SLOTS;       // [EX_MAX_SLOTS]
+    uint64_t* q_empty = bars + 24;         // [2]
+    uint64_t* s_full = bars + 26;          // [EX_S_BUFS]
+    uint64_t* p_full = bars + 29;          // [2]
+    uint64_t* p_empty = bars + 31;         // [2]
+    uint64_t* o_full = bars + 33;
+    uint64_t* drain = bars + 34;
+    uint64_t* wg_max = bars + 35;          // [4] warpgroup exchanges
+    uint64_t* wg_sum = bars + 39;          // [4]
+    uint64_t* wg_vote = bars + 43;         // [4]
     // votes of the warps of a warpgroup, a byte each [tile parity][warpgroup]
-    volatile unsigned char* votes = reinterpret_cast<volatile unsigned char*>(bars + 40);
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 44);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 45);
+    volatile unsigned char* votes = reinterpret_cast<volatile unsigned char*>(bars + 48);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + 52);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 53);
     // row statistics that they exchange: maxima [exchange parity][warpgroup]
-    // [warp][HC], sums [unit parity][..][..][HC][2]
-    float* s_max = reinterpret_cast<float*>(bars + 48);
+    // [warp][HC], sums [unit parity][..][..][1 or 2][HC]
+    float* s_max = reinterpret_cast<float*>(bars + 54);
     float* s_sum = s_max + 8 * R;
-    float* s_fac = s_sum + 16 * R;  // factors of a raise [warp][HC]
+    float* s_fac = s_sum + (C::ONES ? 8 : 16) * R;  // factors of a raise [warp][HC]
     float* s_ref = s_fac + 4 * R;   // negated references [buffer][warpgroup][HC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -411,7 +419,6 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], C::SM_WARPS * 32);
             mbar_init(&p_empty[i], 1);
         }
@@ -420,6 +427,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             mbar_init(&wg_vote[i], 4);
             mbar_init(&wg_sum[i], 128);
         }
+        for (int i = 0; i < EX_S_BUFS; ++i) mbar_init(&s_full[i], 1);
         mbar_init(o_full, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -433,6 +441,15 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
     ex_cum<C::TQ>(P, cum);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
+    if constexpr (C::ONES != 0) {
+        if (warp < 4) {  // bf16 ones: 16 keys (8 columns) for all 128 rows
+            const float one = __uint_as_float(0x3F803F80u);
+            const float v[8] = {one, one, one, one, one, one, one, one};
+            ex_tmem_st<8>(tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::ONES_COL, v);
+            tmem_wait_st();
+        }
+        // read by the issuer only after p_full, which these warps arrive on later
+    }
     // the merge may be scheduled; it waits for this grid before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -507,12 +524,13 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                            in ? 16 : 0);
             }
         };
-        // K of tile x+1 goes before V of tile x, the order of their use; a
-        // tile's rows are looked up while the one before it loads
+        // K of tile x goes before V of tile x - EX_LAG, the order of their use: V
+        // then lands when its weights are ready, and no slot waits for them.
+        // A tile's rows are looked up while the one before it loads.
         ExUnit U;
-        int rows[RL], rows_v[RL], ahead[RL], g_v = 0, t = 0;
+        int rows[RL], ahead[RL], rows_v[EX_LAG][RL], g_v[EX_LAG], t = 0;
         uint32_t unit = 0;
-        for (long long x = x0; x <= x1 && x0 < x1 && ok; ++x) {
+        for (long long x = x0; x < x1 + EX_LAG && x0 < x1 && ok; ++x) {
             if (x < x1) {
                 if (x == x0 || t + 1 >= U.tiles) {
                     ex_unit<C::TQ>(P, cum, x, U);
@@ -528,11 +546,14 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 if (t + 1 < U.tiles) rows_of(U, t + 1, ahead);
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.k, U.g, rows, s);
             }
-            if (x > x0)
-                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.v, g_v, rows_v, s);
+            if (x >= x0 + EX_LAG)
+                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.v, g_v[EX_LAG - 1], rows_v[EX_LAG - 1], s);
 #pragma unroll
-            for (int i = 0; i < RL; ++i) rows_v[i] = rows[i];
-            g_v = U.g;
+            for (int i = EX_LAG - 1; i >= 0; --i) {
+#pragma unroll
+                for (int j = 0; j < RL; ++j) rows_v[i][j] = i > 0 ? rows_v[i - 1][j] : rows[j];
+                g_v[i] = i > 0 ? g_v[i - 1] : U.g;
+            }
         }
         cp_async_wait_all();
     } else if (warp == C::WARP_RECORD) {
@@ -567,27 +588,29 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             const uint32_t v_lo0 = sdesc_lo(smem_u32(sSlots), C::CH_BYTES);  // 64-column chunks
             const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16);
             const uint32_t p_lo0 = sdesc_lo(smem_u32(sP), 16);
-            const uint32_t tmem_o = tmem + 2 * R;
+            constexpr uint32_t IDESC_1 = idesc_bf16(128, R, C::P_ROWS);  // ones: A K-major
+            const uint32_t tmem_o = tmem + C::O_COL;
             uint32_t fill = 0, unit = 0;
             bool ok = true;
             // Unit of the S product and tiles of it still to come; the PV
-            // product runs one tile behind and only needs to know the first
-            // and last tile of a unit.
+            // product runs EX_LAG tiles behind and only needs to know the first
+            // and last tile of a unit (bit i: of the tile i before this one).
             ExUnit U;
             int left = 0;
-            bool first_v = true, last_v = false;  // of the tile that waits for PV
-            for (long long x = x0; x <= x1 && ok; ++x) {
+            uint32_t firsts = 0, lasts = 0;
+            for (long long x = x0; x < x1 + EX_LAG && ok; ++x) {
                 const uint32_t it = static_cast<uint32_t>(x - x0);
-                bool first_s = false, last_s = false;
+                firsts <<= 1;
+                lasts <<= 1;
                 if (x < x1) {
                     if (left == 0) {
                         ex_unit<C::TQ>(P, cum, x, U);
                         const long long end = U.first + U.tiles;
                         left = static_cast<int>((end < x1 ? end : x1) - x);
-                        first_s = true;
+                        firsts |= 1;
                         ++unit;
                     }
-                    last_s = --left == 0;
+                    if (--left == 0) lasts |= 1;
                     const uint32_t qb = (unit - 1) % C::QB;
                     const uint32_t q_lo = q_lo0 + qb * (C::Q_BYTES >> 4);
                     for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
@@ -600,22 +623,33 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         const uint32_t a0 = k_lo0 + slot * (C::SLOT_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < C::SLOT_COLS / 16; ++kk)
-                            umma_ss_lh(tmem + (it & 1) * R,
+                            umma_ss_lh(tmem + (it % EX_S_BUFS) * R,
                                        a0 + (kk / 4) * (C::CH_BYTES >> 4) + (kk % 4) * 2,
                                        q_lo + (s * C::NCH + kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
                                        HI, IDESC_S, (s | kk) != 0);
                         umma_commit(&slot_empty[slot]);
                     }
                     if (!ok) break;
-                    umma_commit(&s_full[it & 1]);
-                    if (last_s) umma_commit(&q_empty[qb]);
+                    umma_commit(&s_full[it % EX_S_BUFS]);
+                    if (lasts & 1) umma_commit(&q_empty[qb]);
                 }
-                if (x > x0) {
-                    const uint32_t pv = it - 1, b = pv & 1;
+                if (x >= x0 + EX_LAG) {
+                    const uint32_t pv = it - EX_LAG, b = pv & 1;
+                    const bool first_v = (firsts >> EX_LAG) & 1;
                     ok = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t p_lo = p_lo0 + b * (C::P_BYTES >> 4);
+                    auto p_step = [&](int kk) -> uint32_t {
+                        return C::P_ROWS ? p_lo + kk * ((16 * 128) >> 4)
+                                         : p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2;
+                    };
+                    if constexpr (C::ONES != 0) {
+#pragma unroll
+                        for (int kk = 0; kk < EX_BN / 16; ++kk)
+                            umma_ts_lh(tmem_o + C::O_BLOCKS * R, tmem + C::ONES_COL, p_step(kk), HI,
+                                       IDESC_1, !(first_v && kk == 0));
+                    }
                     for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
                         const uint32_t slot = fill % C::NS;
                         ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
@@ -626,18 +660,14 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         const uint32_t a0 = v_lo0 + slot * (C::SLOT_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < EX_BN / 16; ++kk)
-                            umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4),
-                                       C::P_ROWS ? p_lo + kk * ((16 * 128) >> 4)
-                                                 : p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
-                                       HI, IDESC_O, !(first_v && kk == 0));
+                            umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4), p_step(kk), HI,
+                                       IDESC_O, !(first_v && kk == 0));
                         umma_commit(&slot_empty[slot]);
                     }
                     if (!ok) break;
                     umma_commit(&p_empty[b]);
-                    if (last_v) umma_commit(o_full);
+                    if ((lasts >> EX_LAG) & 1) umma_commit(o_full);
                 }
-                first_v = first_s;
-                last_v = last_s;
             }
             umma_commit(drain);
             mbar_wait_drain(drain, 0, lim);
@@ -649,7 +679,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         const int key_l = (qd << 5) | lane;                  // key of the tile == TMEM lane
         const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
         const uint32_t s_addr = tmem + lane_addr + wg * HC;
-        const uint32_t o_addr = tmem + lane_addr + 2 * R + wg * HC;
+        const uint32_t o_addr = tmem + lane_addr + C::O_COL + wg * HC;
         // P, keys contiguous: row r, this thread's pair of keys (even, odd) is
         // one 32-bit word. Even lanes store rows c8 + 0..3, odd lanes rows c8 +
         // 4..7; a row's swizzle depends on r mod 8 only, so four addresses
@@ -682,9 +712,12 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
             // sums of the weights of pairs of rows (see pair_row), fp32 ones and
             // the rounded ones
-            float2 l32[HC / 2], lr[HC / 2];
+            float2 l32[HC / 2], lr[C::ONES ? 1 : HC / 2];
 #pragma unroll
-            for (int c = 0; c < HC / 2; ++c) l32[c] = lr[c] = make_float2(0.f, 0.f);
+            for (int c = 0; c < HC / 2; ++c) {
+                l32[c] = make_float2(0.f, 0.f);
+                if constexpr (!C::ONES) lr[c] = make_float2(0.f, 0.f);
+            }
             if constexpr (!FIX) {
                 neg = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
                 if (lane < HC) neg[lane] = -EX_NO_MAX;  // all four warps write the same
@@ -694,12 +727,12 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             // a running reference, also this warp's vote on raising it.
             float next[HC];
             auto peek = [&](int t, uint32_t it) -> bool {
-                const uint32_t b = it & 1;
-                bool k = mbar_wait(&s_full[b], (it >> 1) & 1, abort_flag, lim, SITE_EX_SM);
+                const uint32_t sb = it % EX_S_BUFS;
+                bool k = mbar_wait(&s_full[sb], (it / EX_S_BUFS) & 1, abort_flag, lim, SITE_EX_SM);
                 k = __all_sync(0xffffffffu, k);
                 if (!k) return false;
                 tc_fence_after();
-                ex_scores<HC, FIX>(P, s_addr + b * R, next);
+                ex_scores<HC, FIX>(P, s_addr + sb * R, next);
                 const int k0 = U.lo + t * EX_BN;
                 // an inner tile is seen whole by every row
                 if (k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
@@ -724,7 +757,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                     }
                     const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
                     if (lane == 0) {
-                        votes[(b * C::NWG + wg) * 4 + qd] = raise;
+                        votes[((it & 1) * C::NWG + wg) * 4 + qd] = raise;
                         mbar_arrive(&wg_vote[wg]);
                     }
                 }
@@ -773,8 +806,10 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                             const float fx = fac[pair_row(c, 0)], fy = fac[pair_row(c, 1)];
                             l32[c].x *= fx;
                             l32[c].y *= fy;
-                            lr[c].x *= fx;
-                            lr[c].y *= fy;
+                            if constexpr (!C::ONES) {
+                                lr[c].x *= fx;
+                                lr[c].y *= fy;
+                            }
                         }
                         if (t > t_begin) {  // O must hold every tile before this
                             const uint32_t pv = it - 1;
@@ -784,7 +819,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int o = 0; o < C::O_BLOCKS; ++o) {
+                            for (int o = 0; o < C::O_BLOCKS + C::ONES; ++o) {
 #pragma unroll
                                 for (int c8 = 0; c8 < HC; c8 += 8) {
                                     float a[8];
@@ -823,9 +858,15 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 }
 #pragma unroll
                 for (int c = 0; c < HC; ++c) p[c] = ex2_approx(p[c]);
-                // The P buffer is free: S of this tile was issued after the
-                // product of tile it - 2, and its completion counts that in.
+                // The P buffer is free once the product of tile it - 2 has read it.
+                // S of tile it + 1 was issued after that product, so where it
+                // was awaited above its completion counted that in.
                 const uint32_t p_buf = b * C::P_BYTES;
+                if (t + 1 >= t_end && it >= 2) {
+                    ok = mbar_wait(&p_empty[b], ((it >> 1) - 1) & 1, abort_flag, lim, SITE_EX_SM);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
 #pragma unroll
                 for (int c8 = 0; c8 < HC; c8 += 8) {
                     uint32_t line[4];
@@ -836,7 +877,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         const int i = c8 / 2 + k;
                         const uint32_t own = pack_bf16x2(p[c], p[c + d]);
                         l32[i] = add2(l32[i], make_float2(p[c], p[c + d]));
-                        lr[i] = add_bf16x2_f32(lr[i], own);
+                        if constexpr (!C::ONES) lr[i] = add_bf16x2_f32(lr[i], own);
                         if constexpr (C::P_ROWS) {
                             line[k] = own;
                         } else {
@@ -861,41 +902,49 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             }
             if (!ok) break;
             // row sums over the 128 keys' threads
-            float* ssum = s_sum + ((unit & 1) * C::NWG + wg) * 4 * HC * 2;
+            constexpr int NSUM = C::ONES ? 1 : 2;
+            float* ssum = s_sum + ((unit & 1) * C::NWG + wg) * 4 * NSUM * HC;
             {
                 float v[HC];
-                auto spread = [&](const float2 (&l)[HC / 2]) {
+#pragma unroll
+                for (int c = 0; c < HC / 2; ++c) {
+                    v[pair_row(c, 0)] = l32[c].x;
+                    v[pair_row(c, 1)] = l32[c].y;
+                }
+                const float a = ex_reduce<HC, false>(v);
+                float r = 0.f;
+                if constexpr (!C::ONES) {
 #pragma unroll
                     for (int c = 0; c < HC / 2; ++c) {
-                        v[pair_row(c, 0)] = l[c].x;
-                        v[pair_row(c, 1)] = l[c].y;
+                        v[pair_row(c, 0)] = lr[c].x;
+                        v[pair_row(c, 1)] = lr[c].y;
                     }
-                };
-                spread(l32);
-                const float a = ex_reduce<HC, false>(v);
-                spread(lr);
-                const float r = ex_reduce<HC, false>(v);
+                    r = ex_reduce<HC, false>(v);
+                }
                 if ((lane & (32 / HC - 1)) == 0) {
-                    ssum[(qd * HC + ex_col<HC>(lane)) * 2] = a;
-                    ssum[(qd * HC + ex_col<HC>(lane)) * 2 + 1] = r;
+                    ssum[qd * NSUM * HC + ex_col<HC>(lane)] = a;
+                    if constexpr (!C::ONES) ssum[(qd * NSUM + 1) * HC + ex_col<HC>(lane)] = r;
                 }
                 mbar_arrive(&wg_sum[wg]);
                 ok = mbar_wait(&wg_sum[wg], unit & 1, abort_flag, lim, SITE_EX_SM);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
             }
-            float inv[HC];
-#pragma unroll
-            for (int c = 0; c < HC; ++c) {
-                float l = 0.f;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) l += ssum[(w * HC + c) * 2 + 1];
-                inv[c] = l > 0.f ? rcp_approx(l) : 0.f;
-            }
             ok = mbar_wait(o_full, unit & 1, abort_flag, lim, SITE_EX_SM);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            float lsum[HC];  // sums of the rounded weights
+            if constexpr (C::ONES != 0) {
+                ex_tmem_ld<HC>(o_addr + C::O_BLOCKS * R, lsum);
+            } else {
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    lsum[c] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) lsum[c] += ssum[(w * NSUM + 1) * HC + c];
+                }
+            }
             const bool whole = t_begin == 0 && t_end == U.tiles;
             // a stretch's first segment has slot 0, its last one slot 1
             const size_t ws = static_cast<size_t>(blockIdx.x) * 2 + (unit == 0 ? 0 : 1);
@@ -913,7 +962,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                     if (r >= rows) continue;
                     if (whole)
                         out0[(static_cast<size_t>(r >> 1) * P.H + (r & 1)) * D + dcol] =
-                            __float2bfloat16_rn(a[c] * inv[c]);
+                            __float2bfloat16_rn(lsum[c] > 0.f ? a[c] * rcp_approx(lsum[c]) : 0.f);
                     else
                         P.ws_o[(ws * R + r) * D + dcol] = a[c];
                 }
@@ -922,10 +971,10 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 const int r = wg * HC + key_l;
                 float a = 0.f, l = 0.f, mm = FIX ? P.fixed_ref : EX_NO_MAX;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    a += ssum[(w * HC + key_l) * 2];
-                    l += ssum[(w * HC + key_l) * 2 + 1];
-                }
+                for (int w = 0; w < 4; ++w) a += ssum[w * NSUM * HC + key_l];
+#pragma unroll
+                for (int c = 0; c < HC; ++c)
+                    if (c == key_l) l = lsum[c];
                 if constexpr (!FIX) mm = -neg[key_l];
                 if (!whole) {
                     float* s = P.ws_s + (ws * R + r) * 4;
