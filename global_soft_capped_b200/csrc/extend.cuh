@@ -235,6 +235,17 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* c
     U.qrow = qb + U.t0;
 }
 
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
@@ -580,7 +591,10 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         __syncwarp();
     } else if (warp == C::WARP_MMA) {
         // ------------------------------------------------------ UMMA issuer
-        if (lane == 0 && x0 < x1) {
+        // The whole warp runs the loop (its values stay in uniform registers, as
+        // the instructions want them) and one elected lane issues.
+        if (x0 < x1) {
+            const bool leader = elect_one();
             constexpr uint32_t IDESC_S = idesc_bf16(128, R, false);
             constexpr uint32_t IDESC_O = idesc_bf16(128, R, C::P_ROWS) | (1u << 15);  // A MN-major
             constexpr uint32_t HI = sdesc_hi(1024);
@@ -617,10 +631,12 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         const uint32_t slot = fill % C::NS;
                         ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
                                        SITE_EX_MMA);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = k_lo0 + slot * (C::SLOT_BYTES >> 4);
+                        if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < C::SLOT_COLS / 16; ++kk)
                             umma_ss_lh(tmem + (it % EX_S_BUFS) * R,
@@ -628,15 +644,19 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                                        q_lo + (s * C::NCH + kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
                                        HI, IDESC_S, (s | kk) != 0);
                         umma_commit(&slot_empty[slot]);
+                        }
                     }
                     if (!ok) break;
-                    umma_commit(&s_full[it % EX_S_BUFS]);
-                    if (lasts & 1) umma_commit(&q_empty[qb]);
+                    if (leader) {
+                        umma_commit(&s_full[it % EX_S_BUFS]);
+                        if (lasts & 1) umma_commit(&q_empty[qb]);
+                    }
                 }
                 if (x >= x0 + EX_LAG) {
                     const uint32_t pv = it - EX_LAG, b = pv & 1;
                     const bool first_v = (firsts >> EX_LAG) & 1;
                     ok = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t p_lo = p_lo0 + b * (C::P_BYTES >> 4);
@@ -644,7 +664,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         return C::P_ROWS ? p_lo + kk * ((16 * 128) >> 4)
                                          : p_lo + (kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2;
                     };
-                    if constexpr (C::ONES != 0) {
+                    if (C::ONES != 0 && leader) {
 #pragma unroll
                         for (int kk = 0; kk < EX_BN / 16; ++kk)
                             umma_ts_lh(tmem_o + C::O_BLOCKS * R, tmem + C::ONES_COL, p_step(kk), HI,
@@ -654,23 +674,30 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                         const uint32_t slot = fill % C::NS;
                         ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
                                        SITE_EX_MMA);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = v_lo0 + slot * (C::SLOT_BYTES >> 4);
+                        if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < EX_BN / 16; ++kk)
                             umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4), p_step(kk), HI,
                                        IDESC_O, !(first_v && kk == 0));
                         umma_commit(&slot_empty[slot]);
+                        }
                     }
                     if (!ok) break;
-                    umma_commit(&p_empty[b]);
-                    if ((lasts >> EX_LAG) & 1) umma_commit(o_full);
+                    if (leader) {
+                        umma_commit(&p_empty[b]);
+                        if ((lasts >> EX_LAG) & 1) umma_commit(o_full);
+                    }
                 }
             }
-            umma_commit(drain);
-            mbar_wait_drain(drain, 0, lim);
+            if (leader) {
+                umma_commit(drain);
+                mbar_wait_drain(drain, 0, lim);
+            }
         }
         __syncwarp();
     } else {
