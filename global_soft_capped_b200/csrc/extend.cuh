@@ -485,36 +485,60 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             ok = __all_sync(0xffffffffu, ok);
         };
         const long long rstride = static_cast<long long>(P.Hkv) * D;
-        // this lane's cache rows of key tile `tile`, -1 outside [lo, hi)
-        auto rows_of = [&](const ExUnit& U, int tile, int (&rows)[RL]) {
+        // Block-table entries of this lane's rows of key tile `tile` (loaded a
+        // tile ahead, and only turned into rows when they are needed).
+        auto look_up = [&](const ExUnit& U, int tile, int (&entry)[RL]) {
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
                 const int key = U.lo + tile * EX_BN + pw * RW + i * 32 + lane;
-                rows[i] = -1;
-                if (key < U.hi) {
-                    int b = P.table[static_cast<size_t>(U.seq) * P.max_blocks +
-                                    (key >> P.block_shift)];
-                    b = max(0, min(b, P.num_blocks - 1));
-                    rows[i] = (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
-                }
+                entry[i] = 0;
+                if (key < U.hi)
+                    entry[i] = P.table[static_cast<size_t>(U.seq) * P.max_blocks +
+                                       (key >> P.block_shift)];
+            }
+        };
+        // Cache rows of these entries, -1 outside [lo, hi).
+        auto to_rows = [&](const ExUnit& U, int tile, const int (&entry)[RL], int (&rows)[RL]) {
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                const int key = U.lo + tile * EX_BN + pw * RW + i * 32 + lane;
+                const int b = max(0, min(entry[i], P.num_blocks - 1));
+                rows[i] = (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
+                if (key >= U.hi) rows[i] = -1;
             }
         };
         constexpr int LPR = C::SLOT_COLS / 8;  // lanes per row of a slot
         constexpr int RPI = 32 / LPR;          // rows per instruction
+        constexpr int PER8 = 8 / RPI;          // instructions per 8 rows (the swizzle's period)
+        constexpr int BATCH = 8;
+        const int piece = lane % LPR;          // this lane's 16 bytes of a row
+        uint32_t dst8[PER8];                   // their places in the first rows of a slot
+#pragma unroll
+        for (int i = 0; i < PER8; ++i) {
+            const int r = i * RPI + lane / LPR;
+            dst8[i] = smem_u32(sSlots) + (piece >> 3) * C::CH_BYTES + (pw * RW + r) * 128 +
+                      (((piece & 7) ^ (r & 7)) << 4);
+        }
         auto load_tile = [&](const __nv_bfloat16* cache, int g, const int (&rows)[RL], int s0) {
-            const int c = lane % LPR;
             const uint32_t s = fill % C::NS;
             if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
             if (!ok) return;
-            const uint32_t dst = smem_u32(sSlots) + s * C::SLOT_BYTES + (c >> 3) * C::CH_BYTES;
-            const __nv_bfloat16* src0 = cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + c * 8;
+            const uint32_t slot = s * C::SLOT_BYTES;
+            const __nv_bfloat16* src0 =
+                cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + piece * 8;
+            // in batches: the exchanges of a batch overlap (one by one, their
+            // latency was most of a producer's time)
 #pragma unroll
-            for (int i = 0; i < RW / RPI; ++i) {
-                const int rr = i * RPI + lane / LPR;
-                const int row = __shfl_sync(0xffffffffu, rows[i * RPI / 32], rr & 31);
-                const int r = pw * RW + rr;
-                cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                           src0 + max(row, 0) * rstride, row >= 0 ? 16 : 0);
+            for (int i0 = 0; i0 < RW / RPI; i0 += BATCH) {
+                int row[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    row[i] = __shfl_sync(0xffffffffu, rows[(i0 + i) * RPI / 32],
+                                         ((i0 + i) * RPI + lane / LPR) & 31);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    cp_async16(dst8[(i0 + i) % PER8] + slot + ((i0 + i) / PER8) * 1024,
+                               src0 + max(row[i], 0) * rstride, row[i] >= 0 ? 16 : 0);
             }
             cp_async_arrive(&slot_full[s]);  // counts the unit's Q rows in, too
             ++fill;
@@ -539,22 +563,21 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         // then lands when its weights are ready, and no slot waits for them.
         // A tile's rows are looked up while the one before it loads.
         ExUnit U;
-        int rows[RL], ahead[RL], rows_v[EX_LAG][RL], g_v[EX_LAG], t = 0;
+        int rows[RL], entry[RL], rows_v[EX_LAG][RL], g_v[EX_LAG], t = 0;
         uint32_t unit = 0;
         for (long long x = x0; x < x1 + EX_LAG && x0 < x1 && ok; ++x) {
             if (x < x1) {
                 if (x == x0 || t + 1 >= U.tiles) {
                     ex_unit<C::TQ>(P, cum, x, U);
                     t = static_cast<int>(x - U.first);
-                    rows_of(U, t, rows);
+                    look_up(U, t, entry);
                     load_q(U, unit++);
                     if (!ok) break;
                 } else {
                     ++t;
-#pragma unroll
-                    for (int i = 0; i < RL; ++i) rows[i] = ahead[i];
                 }
-                if (t + 1 < U.tiles) rows_of(U, t + 1, ahead);
+                to_rows(U, t, entry, rows);
+                if (t + 1 < U.tiles) look_up(U, t + 1, entry);
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.k, U.g, rows, s);
             }
             if (x >= x0 + EX_LAG)
