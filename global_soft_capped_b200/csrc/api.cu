@@ -642,8 +642,15 @@ int launch_extend(g2::ExParams& P, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
         return G2ATTN_ERR_CUDA;
+    CUtensorMap mk = {}, mv = {};
+    if (P.use_tma) {
+        const long long rows = static_cast<long long>(P.num_blocks) << P.block_shift;
+        if (!make_map(&mk, P.k, D, rows, P.Hkv, P.box_rows, 1) ||
+            !make_map(&mv, P.v, D, rows, P.Hkv, P.box_rows, 1))
+            return G2ATTN_ERR_CUDA;
+    }
     const int grid = std::min(sms, g2::EX_MAX_CTAS);
-    kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(P);
+    kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(mk, mv, P);
     if (cudaGetLastError() != cudaSuccess) return G2ATTN_ERR_CUDA;
     if (grid == 1) return G2ATTN_OK;  // nothing to join
     // the merge's prologue overlaps the attention kernel's end
@@ -1207,6 +1214,8 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     P.Hkv = Hkv;
     P.window = window;
     P.min_tiles = 1;
+    P.box_rows = std::min(block_size, g2::EX_BN);
+    P.use_tma = block_size >= 8;
     fill_cap(query_scale, softcap, P.k_exp, P.cap_l2, P.scale_l2, P.has_cap);
     const bool fixed = P.has_cap && P.cap_l2 <= g2::PF_FIXED_REF_MAX;
     P.fixed_ref = fixed ? P.cap_l2 - 64.0f : 0.f;

@@ -30,11 +30,12 @@
 //                key; writes P as bf16 into shared memory; at a unit's end
 //                reads O^T (lane = d column) and writes out or the partial.
 //   1 warp       tensor memory, one thread issues the UMMAs.
-//   2 producers  16-byte asynchronous copies of Q, K and V rows into 128-byte-
-//                swizzled tiles, counted on the slots' barriers. Each row's
-//                page is looked up, so pages may be of any size; rows behind the
-//                last visible key are filled with zeros (what the cache holds
-//                there, NaN included, does not matter).
+//   2 producers  K and V into a ring of 128-byte-swizzled tiles. Tiles whose rows
+//                all count come by TMA, a box per page; the others (a sequence's
+//                end, a window's start, pages under 8 rows) and Q by 16-byte
+//                asynchronous copies of rows looked up one by one, with zeros
+//                for rows that no query sees (what the cache holds there, NaN
+//                included, does not matter).
 //   1 warp       writes the CTA's merge record.
 // Softmax: fp32, log2 domain. With the cap the prefill's fixed shift where it
 // fits. Else a reference per row that is the row's maximum over its first tile
@@ -127,6 +128,8 @@ struct ExParams {
     float series_max;    // for |x| up to this (|x / C| <= 1/4)
     int has_cap;
     int min_tiles;   // tiles a CTA takes at least
+    int box_rows;    // rows of a TMA box: min(page, 128), a unit's tiles start at multiples of it
+    int use_tma;     // pages of at least 8 rows (a swizzle atom)
     unsigned long long timeout_ns;
 };
 
@@ -137,6 +140,7 @@ struct ExUnit {
     int qrow;            // packed row of query t0
     int p0;              // position of query t0
     int lo, hi;          // visible keys [lo, hi) of the whole unit
+    int base;            // first key of tile 0
     int tiles;
     long long first;     // number of its first tile in the line
 };
@@ -147,11 +151,12 @@ __device__ __forceinline__ int ex_len(const ExParams& P, int s) {
 }
 
 // Visible keys and tiles (at least one, so that every unit writes its rows) of
-// positions p0 .. p0 + n - 1 of a sequence of length L.
-__device__ __forceinline__ int ex_range(int p0, int n, int L, int window, int& lo, int& hi) {
-    lo = window > 0 ? max(0, p0 - window + 1) : 0;
+// positions p0 .. p0 + n - 1 of a sequence of length L. Tile 0 starts at the box
+// that holds the first visible key.
+__device__ __forceinline__ int ex_range(const ExParams& P, int p0, int n, int L, int& lo, int& hi) {
+    lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
     hi = min(max(0, p0 + n), L);
-    return max(1, (hi - lo + EX_BN - 1) / EX_BN);
+    return max(1, (hi - (lo & -P.box_rows) + EX_BN - 1) / EX_BN);
 }
 
 template <int TQ>
@@ -162,7 +167,7 @@ __device__ __forceinline__ long long ex_seq_tiles(const ExParams& P, int s) {
     long long n = 0;
     for (int t = 0; t < T; t += TQ) {
         int lo, hi;
-        n += ex_range(L - T + t, min(TQ, T - t), L, P.window, lo, hi);
+        n += ex_range(P, L - T + t, min(TQ, T - t), L, lo, hi);
     }
     return n * P.Hkv;
 }
@@ -226,13 +231,14 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* c
     for (U.t0 = 0;; U.t0 += TQ) {
         U.tvalid = min(TQ, T - U.t0);
         U.p0 = L - T + U.t0;
-        U.tiles = ex_range(U.p0, U.tvalid, L, P.window, U.lo, U.hi);
+        U.tiles = ex_range(P, U.p0, U.tvalid, L, U.lo, U.hi);
         if (rem < static_cast<unsigned int>(U.tiles) || U.t0 + TQ >= T) break;
         rem -= U.tiles;
     }
     rem = min(rem, static_cast<unsigned int>(U.tiles) - 1);
     U.first = x - rem;
     U.qrow = qb + U.t0;
+    U.base = U.lo & -P.box_rows;
 }
 
 // True in one lane of the (converged) warp, the same one every time.
@@ -248,6 +254,12 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+// Bytes that asynchronous copies will count on `bar` in this phase.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(bytes)
                  : "memory");
 }
 // Arrives on `bar` once every copy this thread issued so far has landed.
@@ -386,7 +398,9 @@ __device__ __forceinline__ void ex_scores(const ExParams& P, uint32_t addr, floa
 
 // SM = PF_SM_FIXED or PF_SM_CAP (any running max; has_cap tells the cap).
 template <int D, int R, int SM>
-__global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const ExParams P) {
+__global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+    const ExParams P) {
     using C = ExCfg<D, R>;
     constexpr int HC = C::HC;
     constexpr bool FIX = SM == PF_SM_FIXED;
@@ -485,26 +499,45 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             ok = __all_sync(0xffffffffu, ok);
         };
         const long long rstride = static_cast<long long>(P.Hkv) * D;
-        // Block-table entries of this lane's rows of key tile `tile` (loaded a
-        // tile ahead, and only turned into rows when they are needed).
+        // Inner tiles (every row visible to some query) of pages of at least 8
+        // rows: one TMA box per page and 64 columns, box e by lane e of the
+        // first warp.
+        const int per_chunk = EX_BN / P.box_rows;
+        const int box_key = (lane % per_chunk) * P.box_rows;  // first row of this lane's box
+        const int box_chunk = lane / per_chunk;
+        struct Tile {
+            int rows[RL];  // this lane's cache rows, -1: not visible
+            int row;       // first cache row of this lane's box
+            int g;         // KV head
+            bool boxes;    // loaded by TMA
+        };
+        auto by_tma = [&](const ExUnit& U, int tile) -> bool {
+            const int k0 = U.base + tile * EX_BN;
+            return P.use_tma != 0 && k0 >= U.lo && k0 + EX_BN <= U.hi;
+        };
+        // Block-table entries of this lane's rows of a key tile, or of its box
+        // (loaded a tile ahead, and only turned into rows when they are needed).
         auto look_up = [&](const ExUnit& U, int tile, int (&entry)[RL]) {
+            const int* seq = P.table + static_cast<size_t>(U.seq) * P.max_blocks;
+            const int k0 = U.base + tile * EX_BN;
+            if (by_tma(U, tile)) {
+                entry[0] = seq[(k0 + box_key) >> P.block_shift];
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
-                const int key = U.lo + tile * EX_BN + pw * RW + i * 32 + lane;
-                entry[i] = 0;
-                if (key < U.hi)
-                    entry[i] = P.table[static_cast<size_t>(U.seq) * P.max_blocks +
-                                       (key >> P.block_shift)];
+                const int key = k0 + pw * RW + i * 32 + lane;
+                entry[i] = key >= U.lo && key < U.hi ? seq[key >> P.block_shift] : 0;
             }
         };
         // Cache rows of these entries, -1 outside [lo, hi).
         auto to_rows = [&](const ExUnit& U, int tile, const int (&entry)[RL], int (&rows)[RL]) {
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
-                const int key = U.lo + tile * EX_BN + pw * RW + i * 32 + lane;
+                const int key = U.base + tile * EX_BN + pw * RW + i * 32 + lane;
                 const int b = max(0, min(entry[i], P.num_blocks - 1));
                 rows[i] = (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
-                if (key >= U.hi) rows[i] = -1;
+                if (key < U.lo || key >= U.hi) rows[i] = -1;
             }
         };
         constexpr int LPR = C::SLOT_COLS / 8;  // lanes per row of a slot
@@ -519,10 +552,23 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
             dst8[i] = smem_u32(sSlots) + (piece >> 3) * C::CH_BYTES + (pw * RW + r) * 128 +
                       (((piece & 7) ^ (r & 7)) << 4);
         }
-        auto load_tile = [&](const __nv_bfloat16* cache, int g, const int (&rows)[RL], int s0) {
+        auto load_tile = [&](const CUtensorMap* map, const __nv_bfloat16* cache, const Tile& T,
+                             int s0) {
             const uint32_t s = fill % C::NS;
             if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
             if (!ok) return;
+            if (T.boxes) {
+                if (pt == 0) mbar_expect_tx(&slot_full[s], C::SLOT_BYTES);
+                __syncwarp();
+                if (pw == 0 && box_chunk < C::NCH)
+                    tma_load_3d(sSlots + s * C::SLOT_BYTES + box_chunk * C::CH_BYTES + box_key * 128,
+                                map, &slot_full[s], s0 * C::SLOT_COLS + box_chunk * 64, T.row, T.g);
+                cp_async_arrive(&slot_full[s]);
+                ++fill;
+                return;
+            }
+            const int g = T.g;
+            const int (&rows)[RL] = T.rows;
             const uint32_t slot = s * C::SLOT_BYTES;
             const __nv_bfloat16* src0 =
                 cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + piece * 8;
@@ -563,7 +609,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
         // then lands when its weights are ready, and no slot waits for them.
         // A tile's rows are looked up while the one before it loads.
         ExUnit U;
-        int rows[RL], entry[RL], rows_v[EX_LAG][RL], g_v[EX_LAG], t = 0;
+        int entry[RL], t = 0;
+        Tile now, past[EX_LAG];
         uint32_t unit = 0;
         for (long long x = x0; x < x1 + EX_LAG && x0 < x1 && ok; ++x) {
             if (x < x1) {
@@ -576,18 +623,26 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 } else {
                     ++t;
                 }
-                to_rows(U, t, entry, rows);
+                now.g = U.g;
+                now.boxes = by_tma(U, t);
+                if (now.boxes)
+                    now.row = (max(0, min(entry[0], P.num_blocks - 1)) << P.block_shift) +
+                              ((U.base + t * EX_BN + box_key) & ((1 << P.block_shift) - 1));
+                else
+                    to_rows(U, t, entry, now.rows);
                 if (t + 1 < U.tiles) look_up(U, t + 1, entry);
-                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.k, U.g, rows, s);
+                for (int s = 0; s < C::KSL && ok; ++s) load_tile(&map_k, P.k, now, s);
             }
             if (x >= x0 + EX_LAG)
-                for (int s = 0; s < C::KSL && ok; ++s) load_tile(P.v, g_v[EX_LAG - 1], rows_v[EX_LAG - 1], s);
+                for (int s = 0; s < C::KSL && ok; ++s) load_tile(&map_v, P.v, past[EX_LAG - 1], s);
 #pragma unroll
-            for (int i = EX_LAG - 1; i >= 0; --i) {
-#pragma unroll
-                for (int j = 0; j < RL; ++j) rows_v[i][j] = i > 0 ? rows_v[i - 1][j] : rows[j];
-                g_v[i] = i > 0 ? g_v[i - 1] : U.g;
-            }
+            for (int i = EX_LAG - 1; i > 0; --i) past[i] = past[i - 1];
+            past[0] = now;
+        }
+        // every copy has landed before the CTA ends, also after a wait gave up
+        for (uint32_t i = 0; i < static_cast<uint32_t>(C::NS) && i < fill; ++i) {
+            const uint32_t f = fill - 1 - i;
+            if (!mbar_wait_drain(&slot_full[f % C::NS], (f / C::NS) & 1, lim)) break;
         }
         cp_async_wait_all();
     } else if (warp == C::WARP_RECORD) {
@@ -783,7 +838,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(const Ex
                 if (!k) return false;
                 tc_fence_after();
                 ex_scores<HC, FIX>(P, s_addr + sb * R, next);
-                const int k0 = U.lo + t * EX_BN;
+                const int k0 = U.base + t * EX_BN;
                 // an inner tile is seen whole by every row
                 if (k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
                     (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window)) {
