@@ -17,8 +17,9 @@
 // memory once per tile.
 //
 // Work split: units are (sequence, KV head, R/2 positions), each a run of
-// 128-key tiles. All tiles of the launch are numbered in one line and each CTA
-// takes an equal stretch of it, crossing from unit to unit without emptying
+// 128-key tiles. All tiles of the launch are numbered in one line (with some empty
+// places after each unit, for what its end costs) and each CTA takes an equal
+// stretch of it, crossing from unit to unit without emptying
 // its pipeline, so that ragged lengths and few sequences load every SM alike.
 // A unit cut by a stretch's end leaves unnormalised partial results (O, max,
 // sums) in the workspace, at most two per CTA, and extend_merge joins them in
@@ -67,6 +68,10 @@ constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key y
 template <int D, int R>
 struct ExCfg {
     static constexpr int TQ = R / 2;                      // positions per unit
+    // Places in the line of tiles that a unit takes besides its tiles: what its
+    // start and end cost, in tiles (chunks of up to 32 tokens of 24 ragged
+    // sequences, d = 128: 288 us without, 259 with 2, 238 with 4, 235 with 6)
+    static constexpr int UNIT_COST = 768 / D;
     static constexpr int NWG = R == 64 ? 4 : 2;           // softmax warpgroups
     static constexpr int HC = R / NWG;                    // rows per softmax warpgroup
     static constexpr int SM_WARPS = 4 * NWG;
@@ -159,7 +164,7 @@ __device__ __forceinline__ int ex_range(const ExParams& P, int p0, int n, int L,
     return max(1, (hi - (lo & -P.box_rows) + EX_BN - 1) / EX_BN);
 }
 
-template <int TQ>
+template <int TQ, int COST>
 __device__ __forceinline__ long long ex_seq_tiles(const ExParams& P, int s) {
     int qb, T;
     pf_seq_rows(P.cu_q, s, P.total_q, &qb, &T);
@@ -167,16 +172,16 @@ __device__ __forceinline__ long long ex_seq_tiles(const ExParams& P, int s) {
     long long n = 0;
     for (int t = 0; t < T; t += TQ) {
         int lo, hi;
-        n += ex_range(P, L - T + t, min(TQ, T - t), L, lo, hi);
+        n += COST + ex_range(P, L - T + t, min(TQ, T - t), L, lo, hi);
     }
     return n * P.Hkv;
 }
 
-// cum[s] = tiles before sequence s, cum[num_seqs] = all. Whole CTA.
-template <int TQ>
+// cum[s] = places before sequence s, cum[num_seqs] = all. Whole CTA.
+template <int TQ, int COST>
 __device__ __forceinline__ void ex_cum(const ExParams& P, unsigned int* cum) {
     for (int s = threadIdx.x; s < P.num_seqs; s += blockDim.x)
-        cum[s + 1] = static_cast<unsigned int>(min(ex_seq_tiles<TQ>(P, s), EX_MAX_TILES));
+        cum[s + 1] = static_cast<unsigned int>(min(ex_seq_tiles<TQ, COST>(P, s), EX_MAX_TILES));
     if (threadIdx.x == 0) cum[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -203,7 +208,7 @@ __device__ __forceinline__ long long ex_ctas(const ExParams& P, long long all, i
     return n < grid ? n : grid;
 }
 
-// First tile of CTA c's stretch, and the CTA that has a tile.
+// First place of CTA c's stretch, and the CTA that has a place.
 __device__ __forceinline__ long long ex_start(long long c, long long all, long long ctas) {
     return c * all / ctas;
 }
@@ -211,8 +216,9 @@ __device__ __forceinline__ long long ex_owner(long long tile, long long all, lon
     return ((tile + 1) * ctas - 1) / all;
 }
 
-// The unit that holds tile `x` of the line.
-template <int TQ>
+// The unit that holds place `x` of the line (a tile, or the empty places after
+// its last one).
+template <int TQ, int COST>
 __device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* cum, long long x,
                                         ExUnit& U) {
     int lo = 0, hi = P.num_seqs - 1;  // last s with cum[s] <= x
@@ -232,14 +238,40 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* c
         U.tvalid = min(TQ, T - U.t0);
         U.p0 = L - T + U.t0;
         U.tiles = ex_range(P, U.p0, U.tvalid, L, U.lo, U.hi);
-        if (rem < static_cast<unsigned int>(U.tiles) || U.t0 + TQ >= T) break;
-        rem -= U.tiles;
+        if (rem < static_cast<unsigned int>(U.tiles + COST) || U.t0 + TQ >= T) break;
+        rem -= U.tiles + COST;
     }
-    rem = min(rem, static_cast<unsigned int>(U.tiles) - 1);
+    rem = min(rem, static_cast<unsigned int>(U.tiles + COST) - 1);
     U.first = x - rem;
     U.qrow = qb + U.t0;
     U.base = U.lo & -P.box_rows;
 }
+
+// Walks the tiles of a stretch [x0, x1) of the line: unit U, its tile t, of
+// which [begin, end) lie in the stretch.
+template <int TQ, int COST>
+struct ExWalk {
+    ExUnit U;
+    int t, begin, end;
+    bool more;
+    // The first tile at or after place x.
+    __device__ __forceinline__ void seek(const ExParams& P, const unsigned int* cum, long long x,
+                                         long long x1) {
+        for (;;) {
+            more = x < x1;
+            if (!more) return;
+            ex_unit<TQ, COST>(P, cum, x, U);
+            begin = t = static_cast<int>(x - U.first);
+            end = static_cast<int>(min(static_cast<long long>(U.tiles), x1 - U.first));
+            if (t < end) return;
+            x = U.first + U.tiles + COST;
+        }
+    }
+    __device__ __forceinline__ void next_unit(const ExParams& P, const unsigned int* cum,
+                                              long long x1) {
+        seek(P, cum, U.first + U.tiles + COST, x1);
+    }
+};
 
 // True in one lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -463,7 +495,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         tmem_relinquish();
     }
     tc_fence_before();
-    ex_cum<C::TQ>(P, cum);  // ends with a barrier
+    ex_cum<C::TQ, C::UNIT_COST>(P, cum);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
     if constexpr (C::ONES != 0) {
@@ -608,32 +640,34 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         // K of tile x goes before V of tile x - EX_LAG, the order of their use: V
         // then lands when its weights are ready, and no slot waits for them.
         // A tile's rows are looked up while the one before it loads.
-        ExUnit U;
-        int entry[RL], t = 0;
+        int entry[RL];
         Tile now, past[EX_LAG];
         uint32_t unit = 0;
-        for (long long x = x0; x < x1 + EX_LAG && x0 < x1 && ok; ++x) {
-            if (x < x1) {
-                if (x == x0 || t + 1 >= U.tiles) {
-                    ex_unit<C::TQ>(P, cum, x, U);
-                    t = static_cast<int>(x - U.first);
-                    look_up(U, t, entry);
+        ExWalk<C::TQ, C::UNIT_COST> W;
+        W.seek(P, cum, x0, x1);
+        for (int it = 0, left = EX_LAG; left > 0 && ok; ++it) {
+            if (W.more) {
+                const ExUnit& U = W.U;
+                if (W.t == W.begin) {
+                    look_up(U, W.t, entry);
                     load_q(U, unit++);
                     if (!ok) break;
-                } else {
-                    ++t;
                 }
                 now.g = U.g;
-                now.boxes = by_tma(U, t);
+                now.boxes = by_tma(U, W.t);
                 if (now.boxes)
                     now.row = (max(0, min(entry[0], P.num_blocks - 1)) << P.block_shift) +
-                              ((U.base + t * EX_BN + box_key) & ((1 << P.block_shift) - 1));
+                              ((U.base + W.t * EX_BN + box_key) & ((1 << P.block_shift) - 1));
                 else
-                    to_rows(U, t, entry, now.rows);
-                if (t + 1 < U.tiles) look_up(U, t + 1, entry);
+                    to_rows(U, W.t, entry, now.rows);
+                if (W.t + 1 < W.end) look_up(U, W.t + 1, entry);
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(&map_k, P.k, now, s);
+                if (++W.t == W.end) W.next_unit(P, cum, x1);
+            } else {
+                if (it == 0) break;  // an empty stretch
+                --left;
             }
-            if (x >= x0 + EX_LAG)
+            if (it >= EX_LAG)
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(&map_v, P.v, past[EX_LAG - 1], s);
 #pragma unroll
             for (int i = EX_LAG - 1; i > 0; --i) past[i] = past[i - 1];
@@ -653,12 +687,13 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             int4 a = make_int4(-1, 0, 0, 0), b = make_int4(0, 0, 0, 0);
             if (x0 < x1) {
                 ExUnit U;
-                ex_unit<C::TQ>(P, cum, x0, U);
-                if (U.first < x0) {
+                ex_unit<C::TQ, C::UNIT_COST>(P, cum, x0, U);
+                if (U.first < x0 && x0 < U.first + U.tiles) {
                     const int c0 = static_cast<int>(ex_owner(U.first, all, ctas));
                     const int c1 = static_cast<int>(ex_owner(U.first + U.tiles - 1, all, ctas));
                     // c0's partial: its last segment, slot 1 unless also its first
-                    const int slot0 = ex_start(c0, all, ctas) >= U.first ? 0 : 1;
+                    // (c0 starts here or in the empty places before)
+                    const int slot0 = ex_start(c0, all, ctas) >= U.first - C::UNIT_COST ? 0 : 1;
                     a = make_int4(U.qrow, U.g, U.tvalid, slot0);
                     b = make_int4(c0, c1, static_cast<int>(blockIdx.x) - c0 - 1, c1 - c0);
                 }
@@ -684,25 +719,27 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             const uint32_t tmem_o = tmem + C::O_COL;
             uint32_t fill = 0, unit = 0;
             bool ok = true;
-            // Unit of the S product and tiles of it still to come; the PV
-            // product runs EX_LAG tiles behind and only needs to know the first
-            // and last tile of a unit (bit i: of the tile i before this one).
-            ExUnit U;
-            int left = 0;
+            // The PV product runs EX_LAG tiles behind and only needs to know the
+            // first and last tile of a unit (bit i: of the tile i before this one).
             uint32_t firsts = 0, lasts = 0;
-            for (long long x = x0; x < x1 + EX_LAG && ok; ++x) {
-                const uint32_t it = static_cast<uint32_t>(x - x0);
+            ExWalk<C::TQ, C::UNIT_COST> W;
+            W.seek(P, cum, x0, x1);
+            uint32_t it = 0;
+            for (int left = EX_LAG; left > 0 && ok; ++it) {
                 firsts <<= 1;
                 lasts <<= 1;
-                if (x < x1) {
-                    if (left == 0) {
-                        ex_unit<C::TQ>(P, cum, x, U);
-                        const long long end = U.first + U.tiles;
-                        left = static_cast<int>((end < x1 ? end : x1) - x);
+                if (!W.more) {
+                    if (it == 0) break;  // an empty stretch
+                    --left;
+                } else {
+                    if (W.t == W.begin) {
                         firsts |= 1;
                         ++unit;
                     }
-                    if (--left == 0) lasts |= 1;
+                    if (++W.t == W.end) {
+                        lasts |= 1;
+                        W.next_unit(P, cum, x1);
+                    }
                     const uint32_t qb = (unit - 1) % C::QB;
                     const uint32_t q_lo = q_lo0 + qb * (C::Q_BYTES >> 4);
                     for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
@@ -730,7 +767,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         if (lasts & 1) umma_commit(&q_empty[qb]);
                     }
                 }
-                if (x >= x0 + EX_LAG) {
+                if (it >= EX_LAG) {
                     const uint32_t pv = it - EX_LAG, b = pv & 1;
                     const bool first_v = (firsts >> EX_LAG) & 1;
                     ok = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
@@ -808,13 +845,11 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         bool ok = true;
         uint32_t unit = 0, raises = 0, refs = 0;
         float* neg = nullptr;  // this warpgroup's negated references
-        long long x = x0;
-        while (x < x1 && ok) {
-            ExUnit U;
-            ex_unit<C::TQ>(P, cum, x, U);
-            const long long end = U.first + U.tiles;
-            const int t_begin = static_cast<int>(x - U.first);
-            const int t_end = static_cast<int>((end < x1 ? end : x1) - U.first);
+        uint32_t done = 0;  // tiles of the stretch's units before this one
+        ExWalk<C::TQ, C::UNIT_COST> W;
+        for (W.seek(P, cum, x0, x1); W.more && ok; W.next_unit(P, cum, x1)) {
+            const ExUnit& U = W.U;
+            const int t_begin = W.begin, t_end = W.end;
             // sums of the weights of pairs of rows (see pair_row), fp32 ones and
             // the rounded ones
             float2 l32[HC / 2], lr[C::ONES ? 1 : HC / 2];
@@ -868,9 +903,9 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 }
                 return true;
             };
-            ok = peek(t_begin, static_cast<uint32_t>(x - x0));
+            ok = peek(t_begin, done);
             for (int t = t_begin; t < t_end && ok; ++t) {
-                const uint32_t it = static_cast<uint32_t>(x - x0) + (t - t_begin);
+                const uint32_t it = done + (t - t_begin);
                 const uint32_t b = it & 1;
                 if constexpr (!FIX) {
                     ok = mbar_wait(&wg_vote[wg], it & 1, abort_flag, lim, SITE_EX_SM);
@@ -1092,7 +1127,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 }
             }
             tc_fence_before();
-            x += t_end - t_begin;
+            done += t_end - t_begin;
             ++unit;
         }
     }
