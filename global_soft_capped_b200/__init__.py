@@ -134,7 +134,7 @@ def load_library():
     lib.g2attn_extend_paged.restype = I
     lib.g2attn_pages_workspace_size.argtypes = [I, I]
     lib.g2attn_pages_workspace_size.restype = SZ
-    lib.g2attn_pages_grow.argtypes = [P] * 5 + [I] * 4 + [P, SZ, P]
+    lib.g2attn_pages_grow.argtypes = [P] * 7 + [I] * 4 + [P, SZ, P]
     lib.g2attn_pages_grow.restype = I
     lib.g2attn_pages_truncate.argtypes = [P] * 4 + [I] * 4 + [P]
     lib.g2attn_pages_truncate.restype = I
@@ -299,11 +299,13 @@ def g2attn_pages_workspace_size(num_seqs, num_blocks):
     return load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
 
 
-def g2attn_pages_grow(block_table, seq_lens, ref_counts, add, granted, num_seqs, num_blocks,
-                      block_size, max_blocks_per_seq, workspace, workspace_bytes, stream):
+def g2attn_pages_grow(block_table, seq_lens, ref_counts, add, granted, copy_src, copy_dst,
+                      num_seqs, num_blocks, block_size, max_blocks_per_seq, workspace,
+                      workspace_bytes, stream):
     return load_library().g2attn_pages_grow(block_table, seq_lens, ref_counts, add, granted,
-                                            num_seqs, num_blocks, block_size, max_blocks_per_seq,
-                                            workspace, workspace_bytes, stream)
+                                            copy_src, copy_dst, num_seqs, num_blocks, block_size,
+                                            max_blocks_per_seq, workspace, workspace_bytes,
+                                            stream)
 
 
 def g2attn_pages_truncate(block_table, seq_lens, ref_counts, keep, num_seqs, num_blocks,
@@ -693,12 +695,21 @@ def _ints(name, t, n, device, dtype=None):
     return t.data_ptr()
 
 
-def _cache(name, t, like, shape):
+def _cache(name, t, dims, Hkv, d, device):
+    """Pointer of a contiguous bf16 cache (..., Hkv, d)."""
     import torch
-    if t.dtype != torch.bfloat16 or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous bf16 tensor on {like.device}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit {shape}")
+    sh = t.shape
+    if (t.dtype != torch.bfloat16 or t.device != device or len(sh) != dims or sh[-1] != d
+            or sh[-2] != Hkv or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous bf16 tensor of {dims} dimensions on "
+                         f"{device} that ends in (Hkv, d)")
+    return t.data_ptr()
+
+
+def _like_cache(name, t, other):
+    if (t.dtype != other.dtype or t.device != other.device or t.shape != other.shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a tensor like the K cache")
     return t.data_ptr()
 
 
@@ -769,8 +780,7 @@ def rope_append(q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, plan, *, 
     sequence of a packed cache (sum L,Hkv,d); cu_seqlens_q None: one token each."""
     n_seqs = cu_seqlens_k.numel() - 1
     n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
-    kc = _cache("k_cache", k_cache, q, (None, Hkv, d))
-    vc = _cache("v_cache", v_cache, q, tuple(k_cache.shape))
+    kc, vc = _cache("k_cache", k_cache, 3, Hkv, d, q.device), _like_cache("v_cache", v_cache, k_cache)
     _launch("g2attn_rope_append", q.device, stream, (
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
         _ints("cu_seqlens_k", cu_seqlens_k, None, q.device), _plan_args(plan, q.device), n_seqs, n,
@@ -784,8 +794,9 @@ def rope_append_ring(q, k, v, k_ring, v_ring, cu_seqlens_q, seq_lens, plan, *, q
     """:func:`rope_append` into ring caches (n,R,Hkv,d); seq_lens with the new tokens."""
     n_seqs = seq_lens.numel()
     n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
-    kc = _cache("k_ring", k_ring, q, (n_seqs, None, Hkv, d))
-    vc = _cache("v_ring", v_ring, q, tuple(k_ring.shape))
+    kc, vc = _cache("k_ring", k_ring, 4, Hkv, d, q.device), _like_cache("v_ring", v_ring, k_ring)
+    if k_ring.shape[0] != n_seqs:
+        raise ValueError("k_ring: expected one ring per sequence")
     _launch("g2attn_rope_append_ring", q.device, stream, (
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), kc, vc, cu,
         _ints("seq_lens", seq_lens, None, q.device), _plan_args(plan, q.device), n_seqs, n,
@@ -800,8 +811,8 @@ def rope_append_paged(q, k, v, k_blocks, v_blocks, cu_seqlens_q, block_table, se
     int32 (n, max_blocks), seq_lens with the new tokens."""
     n_seqs = seq_lens.numel()
     n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
-    kc = _cache("k_blocks", k_blocks, q, (None, None, Hkv, d))
-    vc = _cache("v_blocks", v_blocks, q, tuple(k_blocks.shape))
+    kc = _cache("k_blocks", k_blocks, 4, Hkv, d, q.device)
+    vc = _like_cache("v_blocks", v_blocks, k_blocks)
     if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
         raise ValueError("block_table: expected one row per sequence")
     _launch("g2attn_rope_append_paged", q.device, stream, (
@@ -830,8 +841,8 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
     if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
         raise ValueError("q: expected a contiguous bf16 CUDA tensor (tokens, H, d)")
     total_q, H, d = q.shape
-    kc = _cache("k_blocks", k_blocks, q, (None, None, None, d))
-    vc = _cache("v_blocks", v_blocks, q, tuple(k_blocks.shape))
+    kc = _cache("k_blocks", k_blocks, 4, k_blocks.shape[-2], d, q.device)
+    vc = _like_cache("v_blocks", v_blocks, k_blocks)
     n = seq_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: expected one row per sequence")
@@ -883,19 +894,27 @@ def _table(block_table, ref_counts):
             block_table.shape[1], ref_counts.numel(), _ints("ref_counts", ref_counts, None, dev))
 
 
-def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, workspace=None,
-               stream=None):
+def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, copies=False,
+               workspace=None, stream=None):
     """Lengthens every sequence by add rows with fresh pages, in place; returns
-    granted (num_seqs,) int32, 0 where the pages ran out."""
+    granted (num_seqs,) int32, 0 where the pages ran out. A sequence that was cut
+    (:func:`pages_truncate`) inside a page which a fork shares needs a copy of it:
+    with ``copies`` the result is (granted, copy_src, copy_dst) for
+    :func:`pages_copy`, without it such a sequence is refused."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    granted = block_table.new_empty(n)
     ws = _pages_ws(workspace, block_table, n, nb)
+    src = dst = None
+    if copies:
+        granted, src, dst = block_table.new_empty((3, n)).unbind(0)
+    else:
+        granted = block_table.new_empty(n)
     _used_on(stream, granted, ws)
     _launch("g2attn_pages_grow", dev, stream, (
         tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev), granted.data_ptr(),
-        n, nb, int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
-    return granted
+        None if src is None else src.data_ptr(), None if dst is None else dst.data_ptr(), n, nb,
+        int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
+    return (granted, src, dst) if copies else granted
 
 
 def pages_truncate(block_table, seq_lens, ref_counts, keep, block_size, *, stream=None):

@@ -584,7 +584,8 @@ int launch_rope(g2::RopeParams& P, bool interleaved, cudaStream_t stream) {
     P.heads_per_group = hpg;
     P.groups = (heads + hpg - 1) / hpg;
     const long long blocks = (slots * P.groups + g2::ROPE_THREADS - 1) / g2::ROPE_THREADS;
-    if (blocks > INT32_MAX) return G2ATTN_ERR_UNSUPPORTED;
+    if (blocks > INT32_MAX || static_cast<long long>(P.tokens) * P.groups > INT32_MAX)
+        return G2ATTN_ERR_UNSUPPORTED;
     const int grid = static_cast<int>(blocks);
     if (interleaved)
         g2::rope_kernel<D, MODE, true><<<grid, g2::ROPE_THREADS, 0, stream>>>(P);
@@ -688,8 +689,7 @@ int launch_extend_rows(int max_T, g2::ExParams& P, bool fixed, cudaStream_t stre
 // Pages
 // ---------------------------------------------------------------------------
 size_t pages_ws_bytes(int num_seqs, int num_blocks) {
-    const size_t a = (static_cast<size_t>(num_seqs) * sizeof(int) + 15) & ~static_cast<size_t>(15);
-    return a + static_cast<size_t>(num_blocks) * sizeof(int);
+    return (2 * static_cast<size_t>(num_seqs) + static_cast<size_t>(num_blocks)) * sizeof(int);
 }
 
 // Arguments that every call on tables has. `ws` is checked where `need_ws`.
@@ -706,9 +706,8 @@ int pages_common(g2::PagesParams& P, const int* table, int* refs, int num_seqs, 
         if (!ws || ws_bytes < pages_ws_bytes(num_seqs, num_blocks)) return G2ATTN_ERR_WORKSPACE;
         if (!aligned16(ws)) return G2ATTN_ERR_MISALIGNED;
         P.ws_base = static_cast<int*>(ws);
-        P.ws_pages = reinterpret_cast<int*>(static_cast<char*>(ws) +
-                                            (pages_ws_bytes(num_seqs, num_blocks) -
-                                             static_cast<size_t>(num_blocks) * sizeof(int)));
+        P.ws_need = P.ws_base + num_seqs;
+        P.ws_pages = P.ws_need + num_seqs;
     }
     P.refs = refs;
     P.num_seqs = num_seqs;
@@ -1184,8 +1183,9 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     int rc = check_common(H, Hkv, d, query_scale, softcap, window);
     if (rc) return rc;
     if (num_seqs > g2::EX_MAX_SEQS) return G2ATTN_ERR_UNSUPPORTED;
+    // (a tile's end may lie one tile past the last key)
     if (static_cast<long long>(num_blocks) * block_size > INT32_MAX ||
-        static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX)
+        static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX - 2 * g2::EX_BN)
         return G2ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_blocks) || !aligned16(v_blocks) || !aligned16(out) ||
         (lse && !aligned16(lse)) || !aligned4(cu_seqlens_q) || !aligned4(block_table) ||
@@ -1226,7 +1226,9 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     P.series[1] = P.scale_l2 * g2::kTanhC1 * us2;
     P.series[2] = P.scale_l2 * g2::kTanhC2 * us2 * us2;
     P.series[3] = P.scale_l2 * g2::kTanhC3 * us2 * us2 * us2;
-    P.series_max = P.has_cap && isfinite(F.poly_acc_max) ? F.poly_acc_max : 0.f;
+    // (off where the coefficients are not finite, also for products of 0)
+    P.series_max =
+        P.has_cap && F.poly_acc_max > 0.f && isfinite(F.poly_acc_max) ? F.poly_acc_max : -1.f;
     P.timeout_ns = wait_limit_ns();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     switch (d) {
@@ -1242,19 +1244,24 @@ size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks) {
 }
 
 int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
-                      int* granted, int num_seqs, int num_blocks, int block_size,
+                      int* granted, int* copy_src, int* copy_dst, int num_seqs, int num_blocks, int block_size,
                       int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
                       g2attn_stream_t stream) {
     g2::PagesParams P{};
     if (!seq_lens || !add || !granted) return G2ATTN_ERR_INVALID_ARG;
+    if ((copy_src == nullptr) != (copy_dst == nullptr)) return G2ATTN_ERR_INVALID_ARG;
     int rc = pages_common(P, block_table, ref_counts, num_seqs, num_blocks, block_size,
                           max_blocks_per_seq, true, workspace, workspace_bytes);
     if (rc) return rc;
-    if (!aligned4(seq_lens) || !aligned4(add) || !aligned4(granted)) return G2ATTN_ERR_MISALIGNED;
+    if (!aligned4(seq_lens) || !aligned4(add) || !aligned4(granted) || !aligned4(copy_src) ||
+        !aligned4(copy_dst))
+        return G2ATTN_ERR_MISALIGNED;
     P.table = block_table;
     P.lens = seq_lens;
     P.arg = add;
     P.granted = granted;
+    P.src = copy_src;
+    P.dst = copy_dst;
     g2::pages_assign<false><<<1, g2::PG_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
     return cudaGetLastError() == cudaSuccess ? G2ATTN_OK : G2ATTN_ERR_CUDA;
 }

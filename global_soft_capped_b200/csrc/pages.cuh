@@ -20,6 +20,7 @@ namespace g2 {
 constexpr int PG_THREADS = 1024;
 constexpr int PG_PER = 16;                       // pages per thread and scan step
 constexpr int PG_STEP = PG_THREADS * PG_PER;
+constexpr int PG_REFUSED = -1;
 constexpr int PG_BASES = 2048;                   // sequences whose ranks stay in shared memory
 constexpr int PG_MAX_CACHES = 128;               // cache pointers per copy launch
 constexpr int PG_COPY_THREADS = 256;
@@ -34,10 +35,11 @@ struct PagesParams {
     int* refs;
     const int* arg;        // grow: rows to add; truncate: rows to keep; fork: parents
     int* granted;          // grow, fork
-    int* src;              // fork, compact: pages to copy (-1: none)
+    int* src;              // fork, compact, grow (may be NULL): pages to copy (-1: none)
     int* dst;
     int* num_live;         // compact
     int* ws_base;          // [num_seqs] rank of a sequence's first fresh page (past PG_BASES)
+    int* ws_need;          // [num_seqs] fresh pages it asks for (past PG_BASES)
     int* ws_pages;         // [num_blocks] fresh pages by rank; compact: new page of a moved one
     int num_seqs, num_blocks, block_shift, max_blocks;
 };
@@ -104,21 +106,30 @@ __device__ __forceinline__ int pg_len(const PagesParams& P, const int* lens, int
                                          static_cast<long long>(P.max_blocks) << P.block_shift)));
 }
 
-// Fresh pages that sequence s asks for (0 when the request cannot be met at
-// all: then `fits` is false).
+// Fresh pages that sequence s asks for; PG_REFUSED when the request cannot be
+// met whatever is free (it then counts as none). Grow: a partly filled last page
+// that other sequences share is replaced by a copy, one page more.
 template <bool FORK>
-__device__ __forceinline__ int pg_need(const PagesParams& P, int s, bool& fits) {
-    fits = true;
+__device__ __forceinline__ int pg_need(const PagesParams& P, int s) {
     if constexpr (FORK) {
         const int p = P.arg[s];
         if (p < 0 || p >= P.num_seqs || p == s) return 0;
         return (pg_len(P, P.lens_in, p) & ((1 << P.block_shift) - 1)) != 0;
     } else {
+        const int add = max(0, P.arg[s]);
         const long long old = pg_len(P, P.lens, s);
         const long long have = pg_pages(old, P.block_shift);
-        const long long want = pg_pages(old + max(0, P.arg[s]), P.block_shift);
-        fits = want <= P.max_blocks;
-        return fits ? static_cast<int>(want - have) : 0;
+        const long long want = pg_pages(old + add, P.block_shift);
+        if (want > P.max_blocks) return PG_REFUSED;
+        int need = static_cast<int>(want - have);
+        if (add > 0 && (old & ((1 << P.block_shift) - 1)) != 0) {
+            const int last = P.table[static_cast<size_t>(s) * P.max_blocks + have - 1];
+            if (last >= 0 && last < P.num_blocks && P.refs[last] > 1) {
+                if (P.src == nullptr) return PG_REFUSED;
+                ++need;
+            }
+        }
+        return need;
     }
 }
 
@@ -130,19 +141,20 @@ template <bool FORK>
 __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) {
     __shared__ int red[33];
     __shared__ long long red64[33];
-    __shared__ int base[PG_BASES];
+    __shared__ int s_base[PG_BASES], s_need[PG_BASES];
     const int tid = threadIdx.x;
+    auto base_of = [&](int s) -> int& { return s < PG_BASES ? s_base[s] : P.ws_base[s]; };
+    auto need_of = [&](int s) -> int& { return s < PG_BASES ? s_need[s] : P.ws_need[s]; };
     long long wanted = 0;  // requests can exceed 32 bits in sum
     for (int b = 0; b < P.num_seqs; b += PG_THREADS) {
         const int s = b + tid;
-        bool fits;
-        const long long need = s < P.num_seqs ? pg_need<FORK>(P, s, fits) : 0;
+        const int need = s < P.num_seqs ? pg_need<FORK>(P, s) : 0;
         long long total;
-        const long long r = wanted + pg_scan(need, red64, total);
+        const long long r = wanted + pg_scan(static_cast<long long>(max(0, need)), red64, total);
         // a rank that no cache has is refused below, whatever it is exactly
         if (s < P.num_seqs) {
-            const int first = static_cast<int>(min(r, 0x7fffffffll));
-            if (s < PG_BASES) base[s] = first; else P.ws_base[s] = first;
+            base_of(s) = static_cast<int>(min(r, 0x7fffffffll));
+            need_of(s) = need;
         }
         wanted += total;
     }
@@ -158,7 +170,17 @@ __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) 
         }
         found += total;
     }
-    __syncthreads();  // ws_base and ws_pages, written by this CTA, are read below
+    __syncthreads();  // ws_pages and what lies past PG_BASES, written by this CTA, are read below
+    auto granted = [&](int base, int need) -> bool {
+        return need == 0 || (need > 0 && static_cast<long long>(base) + need <= found);
+    };
+    for (int s = tid; s < P.num_seqs; s += PG_THREADS) {
+        const int need = need_of(s);
+        const bool ok = granted(base_of(s), need);
+        P.granted[s] = ok;
+        if (P.src != nullptr && (FORK ? !(ok && need > 0) : true)) P.src[s] = P.dst[s] = -1;
+    }
+    __syncthreads();  // (a copy's pair is written over that -1)
     // one thread per fresh page: its sequence is the last one whose rank is not
     // above the page's (of equal ranks the last asks for pages, the others do not)
     const int given = static_cast<int>(min(static_cast<long long>(found), wanted));
@@ -166,33 +188,34 @@ __global__ void __launch_bounds__(PG_THREADS) pages_assign(const PagesParams P) 
         int lo = 0, hi = P.num_seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if ((mid < PG_BASES ? base[mid] : P.ws_base[mid]) <= r) lo = mid; else hi = mid - 1;
+            if (base_of(mid) <= r) lo = mid; else hi = mid - 1;
         }
-        const int first = lo < PG_BASES ? base[lo] : P.ws_base[lo];
-        bool fits;
-        const int need = pg_need<FORK>(P, lo, fits);
-        if (static_cast<long long>(first) + need > found) continue;  // refused
+        const int first = base_of(lo), need = need_of(lo);
+        if (!granted(first, need)) continue;
         const int page = P.ws_pages[r];
         if constexpr (FORK) {
             P.dst[lo] = page;
         } else {
-            const long long have = pg_pages(pg_len(P, P.lens, lo), P.block_shift);
-            P.table[static_cast<size_t>(lo) * P.max_blocks + have + (r - first)] = page;
+            const long long old = pg_len(P, P.lens, lo);
+            const long long have = pg_pages(old, P.block_shift);
+            // rank 0 of one page more than the new rows need: the copy
+            const long long want = pg_pages(old + max(0, P.arg[lo]), P.block_shift);
+            const int copies = need - static_cast<int>(want - have);
+            int* e = P.table + static_cast<size_t>(lo) * P.max_blocks + have - copies + (r - first);
+            if (r - first < copies) {
+                P.src[lo] = *e;
+                P.dst[lo] = page;
+                atomicSub(P.refs + *e, 1);
+            }
+            *e = page;
             P.refs[page] = 1;
         }
     }
-    __syncthreads();  // the lengths are overwritten only now
-    for (int s = tid; s < P.num_seqs; s += PG_THREADS) {
-        bool fits;
-        const int need = pg_need<FORK>(P, s, fits);
-        const int first = s < PG_BASES ? base[s] : P.ws_base[s];
-        const bool ok = fits && (need == 0 || static_cast<long long>(first) + need <= found);
-        P.granted[s] = ok;
-        if constexpr (FORK) {
-            if (!ok || need == 0) P.dst[s] = -1;
-        } else if (ok) {
-            P.lens[s] = pg_len(P, P.lens, s) + max(0, P.arg[s]);
-        }
+    if constexpr (!FORK) {
+        __syncthreads();  // the lengths are overwritten only now
+        for (int s = tid; s < P.num_seqs; s += PG_THREADS)
+            if (granted(base_of(s), need_of(s)))
+                P.lens[s] = pg_len(P, P.lens, s) + max(0, P.arg[s]);
     }
 }
 

@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_MIN_CTAS) rope_kernel(const
     constexpr int SL = D / 16;  // slots of a head
     const long long t = static_cast<long long>(blockIdx.x) * ROPE_THREADS + threadIdx.x;
     const int slot = static_cast<int>(t % SL);
-    const long long unit = t / SL;
-    if (unit >= static_cast<long long>(P.tokens) * P.groups) return;
-    const int token = static_cast<int>(unit / P.groups);
-    const int h0 = static_cast<int>(unit % P.groups) * P.heads_per_group;
+    if (t / SL >= static_cast<long long>(P.tokens) * P.groups) return;
+    const unsigned int unit = static_cast<unsigned int>(t / SL);  // tokens * groups fits 31 bits
+    const int token = static_cast<int>(unit / static_cast<unsigned int>(P.groups));
+    const int h0 = static_cast<int>(unit % static_cast<unsigned int>(P.groups)) * P.heads_per_group;
     const int HK = P.H + P.Hkv;                          // heads that turn
     const int NH = MODE == ROPE_PLAIN ? HK : HK + P.Hkv;  // with the heads of v
     const int h1 = min(NH, h0 + P.heads_per_group);

@@ -382,7 +382,7 @@ G2ATTN_API int g2attn_rope_append_ring(const void* q, const void* k, const void*
  * seq_lens: device int32 [num_seqs], the L_s; block_size a power of two. A token
  * whose table entry lies outside [0, num_blocks) has no row (see above). Pages
  * that several sequences share are not copied: the caller's tables name
- * pages of their own for the rows written here (g2attn_pages_fork leaves them so).
+ * pages of their own for the rows written here (g2attn_pages_grow sees to it).
  */
 G2ATTN_API int g2attn_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
                              void* k_blocks, void* v_blocks, const int* cu_seqlens_q,
@@ -452,16 +452,22 @@ G2ATTN_API size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks);
  * Makes every sequence s longer by add[s] rows (device int32; 0 or less: as it
  * is): fresh pages for the rows past its last page, seq_lens[s] += add[s].
  * Refused when the pages run out or the table row is too short.
+ * A sequence that was cut inside a page which others share must not write into
+ * it: its partly filled page is replaced by a fresh one, whose contents the
+ * caller copies (g2attn_pages_copy) from copy_src[s] to copy_dst[s] before it
+ * appends (device int32 [num_seqs], -1: nothing to copy). Both may be NULL where
+ * that cannot happen (no truncate below a fork); such a sequence is then refused.
  */
 G2ATTN_API int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
-                      int* granted, int num_seqs, int num_blocks, int block_size,
+                      int* granted, int* copy_src, int* copy_dst, int num_seqs, int num_blocks, int block_size,
                       int max_blocks_per_seq, void* workspace, size_t workspace_bytes,
                       g2attn_stream_t stream);
 
 /*
  * Cuts every sequence s to min(its length, max(keep[s], 0)) rows (device int32)
  * and gives the pages behind them back (their counts drop by one; 0: free).
- * keep[s] = 0 frees the sequence; keep[s] >= its length leaves it.
+ * keep[s] = 0 frees the sequence; keep[s] >= its length leaves it. (Grow copies
+ * the page that a cut has left partly filled, if others share it.)
  */
 G2ATTN_API int g2attn_pages_truncate(int* block_table, int* seq_lens, int* ref_counts,
                           const int* keep, int num_seqs, int num_blocks, int block_size,

@@ -110,6 +110,7 @@ EXTEND = dict(q=FAKE, k_blocks=FAKE, v_blocks=FAKE, out=FAKE, lse=None, cu_seqle
     (dict(query_scale=float("inf")), INVALID),
     (dict(H=4), UNSUPPORTED), (dict(d=80), UNSUPPORTED), (dict(num_seqs=1025), UNSUPPORTED),
     (dict(num_blocks=1 << 28), UNSUPPORTED), (dict(max_blocks_per_seq=1 << 28), UNSUPPORTED),
+    (dict(max_blocks_per_seq=(1 << 27) - 1), UNSUPPORTED),  # a tile's end would pass 32 bits
     (dict(out=ODD8), MISALIGNED), (dict(lse=ODD8), MISALIGNED), (dict(seq_lens=ODD2), MISALIGNED),
     (dict(workspace=ODD8), MISALIGNED),
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=64), WORKSPACE),
@@ -129,8 +130,8 @@ def test_extend_workspace_size():
 
 STATE = dict(num_seqs=4, num_blocks=100, block_size=16, max_blocks_per_seq=8)
 WS = dict(workspace=FAKE, workspace_bytes=1 << 20, stream=None)
-GROW = {**dict(block_table=FAKE, seq_lens=FAKE, ref_counts=FAKE, add=FAKE, granted=FAKE), **STATE,
-        **WS}
+GROW = {**dict(block_table=FAKE, seq_lens=FAKE, ref_counts=FAKE, add=FAKE, granted=FAKE,
+               copy_src=FAKE, copy_dst=FAKE), **STATE, **WS}
 CUT = {**dict(block_table=FAKE, seq_lens=FAKE, ref_counts=FAKE, keep=FAKE), **STATE, "stream": None}
 OTHER = ctypes.c_void_p(1 << 21)
 FORK = {**dict(block_table=FAKE, seq_lens=FAKE, parents=FAKE, new_table=OTHER, new_lens=OTHER,

@@ -120,6 +120,24 @@ def test_growing_scores(d, T):
     check(out, ro, lse, rl, f"growing {d}")
 
 
+@pytest.mark.parametrize("cap", [50.0, 0.0, 1e-3])
+@pytest.mark.parametrize("alpha", [-0.1, 0.0])
+def test_odd_scales(alpha, cap):
+    """Negative and zero query scales, a cap that flattens every score."""
+    out, lse, ro, rl = run([(4, 300), (9, 9)], 4, 2, 128, 16, 0, cap, alpha=alpha, seed=12)
+    check(out, ro, lse, rl, f"{alpha} {cap}")
+
+
+def test_zero_keys_and_queries():
+    """Products of exactly 0 (with any cap), rows of equal weights."""
+    def edit(q, k, v, cq, ck):
+        k[::3] = 0
+        q[::2] = 0
+    for cap in (50.0, 0.0, 1e-30, 100.0):
+        out, lse, ro, rl = run([(8, 200), (3, 130)], 4, 2, 64, 16, 0, cap, seed=13, edit=edit)
+        check(out, ro, lse, rl, f"zeros {cap}")
+
+
 def test_peaked_scores_with_the_cap():
     out, lse, ro, rl = run([(4, 1000), (16, 130)], 4, 2, 128, 16, 0, 50.0, alpha=3.0, seed=2)
     check(out, ro, lse, rl, "peaked")

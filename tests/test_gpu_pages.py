@@ -30,23 +30,34 @@ class Model:
     def free(self):
         return [int(p) for p in np.flatnonzero(self.refs == 0)]
 
-    def grow(self, add):
-        free, asked = self.free(), 0
-        granted = np.zeros(len(add), dtype=np.int32)
+    def grow(self, add, copies=False):
+        free, asked, n = self.free(), 0, len(add)
+        granted = np.zeros(n, dtype=np.int32)
+        src, dst = -np.ones(n, dtype=np.int32), -np.ones(n, dtype=np.int32)
+        counts = self.refs.copy()  # shared or not, before anything changes
         for s, a in enumerate(add):
             a = max(0, int(a))
             have, want = -(-int(self.lens[s]) // self.bs), -(-(int(self.lens[s]) + a) // self.bs)
             if want > self.cols:
                 continue
-            asked += want - have
-            if want > have and asked > len(free):
+            copy = a > 0 and self.lens[s] % self.bs != 0 and counts[self.table[s, have - 1]] > 1
+            if copy and not copies:
+                continue
+            need = want - have + copy
+            asked += need
+            if need and asked > len(free):
                 continue
             granted[s] = 1
-            for i, c in enumerate(range(have, want)):
-                page = free[asked - (want - have) + i]
+            pages = free[asked - need:asked]
+            if copy:
+                src[s], dst[s] = self.table[s, have - 1], pages[0]
+                self.refs[src[s]] -= 1
+                self.table[s, have - 1], self.refs[dst[s]] = dst[s], 1
+                pages = pages[1:]
+            for page, c in zip(pages, range(have, want)):
                 self.table[s, c], self.refs[page] = page, 1
             self.lens[s] += a
-        return granted
+        return (granted, src, dst) if copies else granted
 
     def truncate(self, keep):
         for s, k in enumerate(keep):
@@ -120,9 +131,11 @@ class Pair:
         for a, b in ((self.table, self.m.table), (self.lens, self.m.lens), (self.refs, self.m.refs)):
             assert np.array_equal(a.cpu().numpy(), b)
 
-    def grow(self, add):
-        got = g2.pages_grow(self.table, self.lens, self.refs, dev(add), self.bs)
-        assert np.array_equal(got.cpu().numpy(), self.m.grow(add))
+    def grow(self, add, copies=False):
+        got = g2.pages_grow(self.table, self.lens, self.refs, dev(add), self.bs, copies=copies)
+        want = self.m.grow(add, copies)
+        for a, b in zip(got, want) if copies else [(got, want)]:
+            assert np.array_equal(a.cpu().numpy(), b)
         self.same()
         return got
 
@@ -164,7 +177,7 @@ def test_random_life(n, cols, pages, bs):
         what = rng.integers(0, 5)
         if what <= 1 or step == 0:
             add = rng.integers(-2, max(2, top // 3), n) * (rng.random(n) < 0.7)
-            p.grow(add)
+            p.grow(add, copies=bool(rng.random() < 0.6))
         elif what == 2:
             keep = np.where(rng.random(n) < 0.5, rng.integers(-1, top + 2, n), top)
             p.truncate(keep)
@@ -238,6 +251,20 @@ def test_forks_of_one_parent_and_swaps():
     assert (granted == 1).all()
     assert src.tolist()[1] == src.tolist()[2] >= 0 and dst.tolist()[1] != dst.tolist()[2]
     assert src.tolist()[5] == -1 and src.tolist()[0] == -1
+
+
+def test_growing_after_a_cut_inside_a_shared_page():
+    """Two sequences share two full pages; both are cut inside the second one."""
+    p = Pair(3, 4, 10, 8)
+    p.grow([16, 0, 0])
+    p.fork([0, 0, 0])                                    # three rows, two shared pages
+    p.truncate([12, 11, 16])
+    assert p.grow([3, 3, 1]).tolist() == [0, 0, 1]       # would write into the shared page
+    granted, src, dst = p.grow([3, 6, 0], copies=True)
+    assert granted.tolist() == [1, 1, 1] and src.tolist() == [1, 1, -1]
+    assert dst.tolist() == [3, 4, -1] and p.refs.tolist()[:6] == [3, 1, 1, 1, 1, 1]
+    granted, src, dst = p.grow([1, 1, 1], copies=True)   # nothing is shared now
+    assert src.tolist() == dst.tolist() == [-1, -1, -1]
 
 
 def test_fork_refused_without_pages():
