@@ -387,8 +387,8 @@ __device__ __forceinline__ int ex_col(int lane) {
     return N == 32 ? lane : (N == 16 ? lane >> 1 : lane >> 2);
 }
 
-// Scores in log2 units, less the fixed shift, of this lane's key and HC rows, from the
-// raw products in TMEM.
+// Of this lane's key and HC rows, from the products in TMEM: with the cap scores
+// in log2 units, less the fixed shift; without it the products as they are.
 template <int HC, bool FIX>
 __device__ __forceinline__ void ex_scores(const ExParams& P, uint32_t addr, float (&p)[HC]) {
     ex_tmem_ld<HC>(addr, p);
@@ -417,13 +417,6 @@ __device__ __forceinline__ void ex_scores(const ExParams& P, uint32_t addr, floa
             for (int c = 0; c < HC; ++c)
                 p[c] = fmaf(-2.0f * P.cap_l2, rcp_approx(1.0f + ex2_approx(p[c] * P.k_exp)),
                             P.cap_l2 + sh);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < HC; c += 2) {
-            const float2 y = mul2(make_float2(p[c], p[c + 1]), make_float2(P.scale_l2, P.scale_l2));
-            p[c] = y.x;
-            p[c + 1] = y.y;
         }
     }
 }
@@ -845,6 +838,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         bool ok = true;
         uint32_t unit = 0, raises = 0, refs = 0;
         float* neg = nullptr;  // this warpgroup's negated references
+        // what turns a score into log2 units (see ex_scores)
+        const float unit_l2 = P.has_cap ? 1.0f : P.scale_l2;
         uint32_t done = 0;  // tiles of the stretch's units before this one
         ExWalk<C::TQ, C::UNIT_COST> W;
         for (W.seek(P, cum, x0, x1); W.more && ok; W.next_unit(P, cum, x1)) {
@@ -858,13 +853,16 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 l32[c] = make_float2(0.f, 0.f);
                 if constexpr (!C::ONES) lr[c] = make_float2(0.f, 0.f);
             }
+            float limit = EX_NO_MAX;  // scores above this raise the references
             if constexpr (!FIX) {
                 neg = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
                 if (lane < HC) neg[lane] = -EX_NO_MAX;  // all four warps write the same
                 __syncwarp();
             }
-            // Scores of tile t in log2 units (less the fixed shift), masked. With
-            // a running reference, also this warp's vote on raising it.
+            // Waits for tile t's scores and reads them; with a running reference
+            // also this warp's vote on raising it: its largest score (also of
+            // keys that a row does not see, which errs on the safe side) against
+            // the lowest reference of the warpgroup's rows.
             float next[HC];
             auto peek = [&](int t, uint32_t it) -> bool {
                 const uint32_t sb = it % EX_S_BUFS;
@@ -873,35 +871,37 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 if (!k) return false;
                 tc_fence_after();
                 ex_scores<HC, FIX>(P, s_addr + sb * R, next);
-                const int k0 = U.base + t * EX_BN;
-                // an inner tile is seen whole by every row
-                if (k0 + EX_BN - 1 > U.p0 || k0 + EX_BN > U.hi ||
-                    (P.window > 0 && U.p0 + U.tvalid - 1 - k0 >= P.window)) {
-                    const int key = k0 + key_l;
-#pragma unroll
-                    for (int c = 0; c < HC; ++c) {
-                        const int pos = U.p0 + ((wg * HC + c) >> 1);
-                        if (key > pos || key >= U.hi || (P.window > 0 && pos - key >= P.window))
-                            next[c] = -INFINITY;
-                    }
-                }
                 if constexpr (!FIX) {
-                    float top = -INFINITY;
+                    float top = next[0], low = next[0];
 #pragma unroll
-                    for (int c = 0; c < HC; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(neg + c);
-                        const float2 u = add2(make_float2(next[c], next[c + 1]), make_float2(f.x, f.y));
-                        const float2 v =
-                            add2(make_float2(next[c + 2], next[c + 3]), make_float2(f.z, f.w));
-                        top = fmax3f(top, fmaxf(u.x, u.y), fmaxf(v.x, v.y));
+                    for (int c = 1; c + 1 < HC; c += 2) top = fmax3f(top, next[c], next[c + 1]);
+                    top = fmaxf(top, next[HC - 1]) * unit_l2;
+                    if (unit_l2 < 0.f) {
+#pragma unroll
+                        for (int c = 1; c < HC; ++c) low = fminf(low, next[c]);
+                        top = low * unit_l2;
                     }
-                    const bool raise = __any_sync(0xffffffffu, top > EX_RAISE_LOG2);
+                    const bool raise = __any_sync(0xffffffffu, top > limit);
                     if (lane == 0) {
                         votes[((it & 1) * C::NWG + wg) * 4 + qd] = raise;
                         mbar_arrive(&wg_vote[wg]);
                     }
                 }
                 return true;
+            };
+            // Scores that a row does not see, in the tiles where there are any.
+            auto mask = [&](int t, float (&p)[HC]) {
+                const int k0 = U.base + t * EX_BN, key = k0 + key_l;
+                // an inner tile is seen whole by every row
+                if (k0 + EX_BN - 1 <= U.p0 && k0 + EX_BN <= U.hi &&
+                    (P.window == 0 || U.p0 + U.tvalid - 1 - k0 < P.window))
+                    return;
+#pragma unroll
+                for (int c = 0; c < HC; ++c) {
+                    const int pos = U.p0 + ((wg * HC + c) >> 1);
+                    if (key > pos || key >= U.hi || (P.window > 0 && pos - key >= P.window))
+                        p[c] = -INFINITY;
+                }
             };
             ok = peek(t_begin, done);
             for (int t = t_begin; t < t_end && ok; ++t) {
@@ -917,7 +917,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         {
                             float mx[HC];
 #pragma unroll
-                            for (int c = 0; c < HC; ++c) mx[c] = next[c];
+                            for (int c = 0; c < HC; ++c) mx[c] = next[c] * unit_l2;
+                            mask(t, mx);
                             const float w = ex_reduce<HC, true>(mx);
                             if ((lane & (32 / HC - 1)) == 0) st[qd * HC + ex_col<HC>(lane)] = w;
                         }
@@ -941,6 +942,12 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         }
                         neg = to;
                         __syncwarp();
+                        // the lowest reference, rows that only fill the unit aside
+                        limit = lane < HC && wg * HC + lane < 2 * U.tvalid ? -neg[lane] : INFINITY;
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            limit = fminf(limit, __shfl_xor_sync(0xffffffffu, limit, o));
+                        limit += EX_RAISE_LOG2;
 #pragma unroll
                         for (int c = 0; c < HC / 2; ++c) {
                             const float fx = fac[pair_row(c, 0)], fy = fac[pair_row(c, 1)];
@@ -982,15 +989,18 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         for (int k = 0; k < 4; ++k) p[c + k] = next[c + k];
                     } else {
                         const float4 f = *reinterpret_cast<const float4*>(neg + c);
-                        const float2 u = add2(make_float2(next[c], next[c + 1]), make_float2(f.x, f.y));
+                        const float2 by = make_float2(unit_l2, unit_l2);
+                        const float2 u =
+                            fma2(make_float2(next[c], next[c + 1]), by, make_float2(f.x, f.y));
                         const float2 v =
-                            add2(make_float2(next[c + 2], next[c + 3]), make_float2(f.z, f.w));
+                            fma2(make_float2(next[c + 2], next[c + 3]), by, make_float2(f.z, f.w));
                         p[c] = u.x;
                         p[c + 1] = u.y;
                         p[c + 2] = v.x;
                         p[c + 3] = v.y;
                     }
                 }
+                mask(t, p);
                 // the next tile's scores (and vote) while this one's weights go out
                 if (t + 1 < t_end) {
                     ok = peek(t + 1, it + 1);
