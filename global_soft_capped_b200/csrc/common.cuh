@@ -16,14 +16,12 @@ namespace g2 {
 // ---------------------------------------------------------------------------
 // Sticky device error word. Bit 0: a bounded wait gave up. Bit 1
 // (DEVERR_CACHE_LEN): a decode sequence needed more splits than the caller's
-// max_cache_len planned for. Bit 2 (DEVERR_CACHE_ROW): a token to be appended
-// had no row in its cache and was dropped. The upper 16 bits keep the code of the first
+// max_cache_len planned for. The upper 16 bits keep the code of the first
 // wait site that gave up (diagnostics only).
 // ---------------------------------------------------------------------------
 __device__ unsigned int g_device_error = 0;
 constexpr unsigned int DEVERR_TIMEOUT = 1u;
 constexpr unsigned int DEVERR_CACHE_LEN = 2u;
-constexpr unsigned int DEVERR_CACHE_ROW = 4u;
 
 enum WaitSite : unsigned int {
     SITE_SELFTEST = 1,
@@ -47,9 +45,6 @@ enum WaitSite : unsigned int {
     SITE_EPI_O_DONE = 19,   // forward epilogue: the unit's last PV completed
     SITE_EPI_STATS = 20,    // forward epilogue: row statistics handed over
     SITE_SCHED = 21,        // forward, dynamic schedule: a unit published / released
-    SITE_EX_PROD = 22,      // chunk attention producers: slot or Q buffer free
-    SITE_EX_MMA = 23,       // chunk attention issuer: slot or weights ready
-    SITE_EX_SM = 24,        // chunk attention softmax: S, P buffer, O or the other warps
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

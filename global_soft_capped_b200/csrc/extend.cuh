@@ -52,6 +52,11 @@
 
 namespace g2 {
 
+// wait sites of the device error word, after those of the other kernels
+constexpr unsigned int SITE_EX_PROD = 22;  // producers: slot or Q buffer free
+constexpr unsigned int SITE_EX_MMA = 23;   // issuer: slot or weights ready
+constexpr unsigned int SITE_EX_SM = 24;    // softmax: S, P buffer, O or the other warps
+
 constexpr int EX_BN = 128;            // keys per tile
 constexpr int EX_PROD_WARPS = 2;
 constexpr int EX_S_BUFS = 3;          // S tiles in tensor memory

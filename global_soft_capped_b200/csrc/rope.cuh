@@ -26,6 +26,11 @@
 
 namespace g2 {
 
+// Bit 2 of the sticky device error word (bits 0 and 1: a wait that gave up, a
+// decode split plan that was too short): a token to be appended had no row in
+// its cache and was dropped.
+constexpr unsigned int DEVERR_CACHE_ROW = 4u;
+
 constexpr int ROPE_THREADS = 128;
 constexpr int ROPE_MIN_CTAS = 6;   // 768 threads of up to 85 registers per SM
 constexpr int ROPE_UNROLL = 4;     // heads in flight per thread (128 bytes of loads)
