@@ -1213,7 +1213,6 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     P.H = H;
     P.Hkv = Hkv;
     P.window = window;
-    P.min_tiles = 1;
     P.box_rows = std::min(block_size, g2::EX_BN);
     P.use_tma = block_size >= 8;
     fill_cap(query_scale, softcap, P.k_exp, P.cap_l2, P.scale_l2, P.has_cap);

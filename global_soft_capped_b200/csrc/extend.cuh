@@ -137,7 +137,6 @@ struct ExParams {
     float series[4];     // capped score in log2 units = x (s0 + s1 x^2 + s2 x^4 + s3 x^6)
     float series_max;    // for |x| up to this (|x / C| <= 1/4)
     int has_cap;
-    int min_tiles;   // tiles a CTA takes at least
     int box_rows;    // rows of a TMA box: min(page, 128), a unit's tiles start at multiples of it
     int use_tma;     // pages of at least 8 rows (a swizzle atom)
     unsigned long long timeout_ns;
@@ -146,7 +145,8 @@ struct ExParams {
 // A unit and its stretch of the line of tiles.
 struct ExUnit {
     int seq, g, t0;      // first query row of the unit within its sequence
-    int tvalid;          // its query rows (1 .. TQ)
+    int T, L, q0;        // the sequence's queries and keys, packed row of its first query
+    int tvalid;          // the unit's query rows (1 .. TQ)
     int qrow;            // packed row of query t0
     int p0;              // position of query t0
     int lo, hi;          // visible keys [lo, hi) of the whole unit
@@ -207,10 +207,10 @@ __device__ __forceinline__ void ex_cum(const ExParams& P, unsigned int* cum) {
     __syncthreads();
 }
 
-// CTAs that take part: every one of them gets at least one tile.
-__device__ __forceinline__ long long ex_ctas(const ExParams& P, long long all, int grid) {
-    const long long n = (all + P.min_tiles - 1) / P.min_tiles;
-    return n < grid ? n : grid;
+// CTAs that take part: every one of them gets at least one place (more than one,
+// fewer CTAs, measured slower on short caches and no different on long ones).
+__device__ __forceinline__ long long ex_ctas(long long all, int grid) {
+    return all < grid ? all : grid;
 }
 
 // First place of CTA c's stretch, and the CTA that has a place.
@@ -219,6 +219,22 @@ __device__ __forceinline__ long long ex_start(long long c, long long all, long l
 }
 __device__ __forceinline__ long long ex_owner(long long tile, long long all, long long ctas) {
     return ((tile + 1) * ctas - 1) / all;
+}
+
+__device__ __forceinline__ void ex_load_seq(const ExParams& P, int s, ExUnit& U) {
+    U.seq = s;
+    pf_seq_rows(P.cu_q, s, P.total_q, &U.q0, &U.T);
+    U.L = ex_len(P, s);
+}
+
+// The rest of U from seq, g and t0.
+template <int TQ>
+__device__ __forceinline__ void ex_fill_unit(const ExParams& P, ExUnit& U) {
+    U.tvalid = min(TQ, U.T - U.t0);
+    U.p0 = U.L - U.T + U.t0;
+    U.tiles = ex_range(P, U.p0, U.tvalid, U.L, U.lo, U.hi);
+    U.qrow = U.q0 + U.t0;
+    U.base = U.lo & -P.box_rows;
 }
 
 // The unit that holds place `x` of the line (a tile, or the empty places after
@@ -231,25 +247,17 @@ __device__ __forceinline__ void ex_unit(const ExParams& P, const unsigned int* c
         const int mid = (lo + hi + 1) >> 1;
         if (cum[mid] <= x) lo = mid; else hi = mid - 1;
     }
-    U.seq = lo;
-    int qb, T;
-    pf_seq_rows(P.cu_q, lo, P.total_q, &qb, &T);
-    const int L = ex_len(P, lo);
+    ex_load_seq(P, lo, U);
     const unsigned int n = cum[lo + 1] - cum[lo], at = static_cast<unsigned int>(x) - cum[lo];
     const unsigned int per_g = max(1u, n / static_cast<unsigned int>(P.Hkv));
     U.g = static_cast<int>(min(at / per_g, static_cast<unsigned int>(P.Hkv) - 1));
     unsigned int rem = at - U.g * per_g;
     for (U.t0 = 0;; U.t0 += TQ) {
-        U.tvalid = min(TQ, T - U.t0);
-        U.p0 = L - T + U.t0;
-        U.tiles = ex_range(P, U.p0, U.tvalid, L, U.lo, U.hi);
-        if (rem < static_cast<unsigned int>(U.tiles + COST) || U.t0 + TQ >= T) break;
+        ex_fill_unit<TQ>(P, U);
+        if (rem < static_cast<unsigned int>(U.tiles + COST) || U.t0 + TQ >= U.T) break;
         rem -= U.tiles + COST;
     }
-    rem = min(rem, static_cast<unsigned int>(U.tiles + COST) - 1);
-    U.first = x - rem;
-    U.qrow = qb + U.t0;
-    U.base = U.lo & -P.box_rows;
+    U.first = x - min(rem, static_cast<unsigned int>(U.tiles + COST) - 1);
 }
 
 // Walks the tiles of a stretch [x0, x1) of the line: unit U, its tile t, of
@@ -259,22 +267,37 @@ struct ExWalk {
     ExUnit U;
     int t, begin, end;
     bool more;
-    // The first tile at or after place x.
-    __device__ __forceinline__ void seek(const ExParams& P, const unsigned int* cum, long long x,
-                                         long long x1) {
-        for (;;) {
-            more = x < x1;
-            if (!more) return;
-            ex_unit<TQ, COST>(P, cum, x, U);
-            begin = t = static_cast<int>(x - U.first);
-            end = static_cast<int>(min(static_cast<long long>(U.tiles), x1 - U.first));
-            if (t < end) return;
-            x = U.first + U.tiles + COST;
-        }
+    __device__ __forceinline__ void start(const ExParams& P, const unsigned int* cum, long long x0,
+                                          long long x1) {
+        more = x0 < x1;
+        if (!more) return;
+        ex_unit<TQ, COST>(P, cum, x0, U);
+        begin = t = static_cast<int>(x0 - U.first);
+        end = static_cast<int>(min(static_cast<long long>(U.tiles), x1 - U.first));
+        if (t >= end) next_unit(P, cum, x1);  // in the empty places
     }
+    // Units follow one another by position, KV head, sequence (a search for
+    // each would cost more than a short unit's tiles).
     __device__ __forceinline__ void next_unit(const ExParams& P, const unsigned int* cum,
                                               long long x1) {
-        seek(P, cum, U.first + U.tiles + COST, x1);
+        U.first += U.tiles + COST;
+        more = U.first < x1;
+        if (!more) return;
+        U.t0 += TQ;
+        if (U.t0 >= U.T) {
+            U.t0 = 0;
+            if (++U.g == P.Hkv) {
+                U.g = 0;
+                int s = U.seq + 1;
+                while (s < P.num_seqs && cum[s + 1] == cum[s]) ++s;  // without queries
+                more = s < P.num_seqs;
+                if (!more) return;
+                ex_load_seq(P, s, U);
+            }
+        }
+        ex_fill_unit<TQ>(P, U);
+        begin = t = 0;
+        end = static_cast<int>(min(static_cast<long long>(U.tiles), x1 - U.first));
     }
 };
 
@@ -298,6 +321,18 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
                  "r"(bytes)
                  : "memory");
+}
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // Arrives on `bar` once every copy this thread issued so far has landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -509,7 +544,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const long long all = cum[P.num_seqs];
-    const long long ctas = ex_ctas(P, all, gridDim.x);
+    const long long ctas = ex_ctas(all, gridDim.x);
     long long x0 = 0, x1 = 0;
     if (static_cast<long long>(blockIdx.x) < ctas) {
         x0 = ex_start(blockIdx.x, all, ctas);
@@ -642,7 +677,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         Tile now, past[EX_LAG];
         uint32_t unit = 0;
         ExWalk<C::TQ, C::UNIT_COST> W;
-        W.seek(P, cum, x0, x1);
+        W.start(P, cum, x0, x1);
         for (int it = 0, left = EX_LAG; left > 0 && ok; ++it) {
             if (W.more) {
                 const ExUnit& U = W.U;
@@ -721,12 +756,13 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             // first and last tile of a unit (bit i: of the tile i before this one).
             uint32_t firsts = 0, lasts = 0;
             ExWalk<C::TQ, C::UNIT_COST> W;
-            W.seek(P, cum, x0, x1);
+            W.start(P, cum, x0, x1);
             uint32_t it = 0;
             for (int left = EX_LAG; left > 0 && ok; ++it) {
                 firsts <<= 1;
                 lasts <<= 1;
-                if (!W.more) {
+                const bool has_s = W.more;
+                if (!has_s) {
                     if (it == 0) break;  // an empty stretch
                     --left;
                 } else {
@@ -738,39 +774,46 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         lasts |= 1;
                         W.next_unit(P, cum, x1);
                     }
+                }
+                // slots in the order of their filling: K of this tile, V of the
+                // tile EX_LAG before
+                const uint32_t k_fill = fill, v_fill = fill + (has_s ? C::KSL : 0);
+                auto do_s = [&]() -> bool {
                     const uint32_t qb = (unit - 1) % C::QB;
                     const uint32_t q_lo = q_lo0 + qb * (C::Q_BYTES >> 4);
-                    for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
-                        const uint32_t slot = fill % C::NS;
-                        ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
-                                       SITE_EX_MMA);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
+#pragma unroll
+                    for (int s = 0; s < C::KSL; ++s) {
+                        const uint32_t f = k_fill + s, slot = f % C::NS;
+                        bool k = mbar_wait(&slot_full[slot], (f / C::NS) & 1, abort_flag, lim,
+                                           SITE_EX_MMA);
+                        k = __all_sync(0xffffffffu, k);
+                        if (!k) return false;
                         fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = k_lo0 + slot * (C::SLOT_BYTES >> 4);
                         if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < C::SLOT_COLS / 16; ++kk)
-                            umma_ss_lh(tmem + (it % EX_S_BUFS) * R,
-                                       a0 + (kk / 4) * (C::CH_BYTES >> 4) + (kk % 4) * 2,
-                                       q_lo + (s * C::NCH + kk / 4) * ((R * 128) >> 4) + (kk % 4) * 2,
-                                       HI, IDESC_S, (s | kk) != 0);
-                        umma_commit(&slot_empty[slot]);
+                            for (int kk = 0; kk < C::SLOT_COLS / 16; ++kk)
+                                umma_ss_lh(tmem + (it % EX_S_BUFS) * R,
+                                           a0 + (kk / 4) * (C::CH_BYTES >> 4) + (kk % 4) * 2,
+                                           q_lo + (s * C::NCH + kk / 4) * ((R * 128) >> 4) +
+                                               (kk % 4) * 2,
+                                           HI, IDESC_S, (s | kk) != 0);
+                            umma_commit(&slot_empty[slot]);
                         }
                     }
-                    if (!ok) break;
                     if (leader) {
                         umma_commit(&s_full[it % EX_S_BUFS]);
                         if (lasts & 1) umma_commit(&q_empty[qb]);
                     }
-                }
-                if (it >= EX_LAG) {
-                    const uint32_t pv = it - EX_LAG, b = pv & 1;
+                    return true;
+                };
+                const uint32_t pv = it - EX_LAG, b = pv & 1;
+                auto do_pv = [&]() -> bool {
                     const bool first_v = (firsts >> EX_LAG) & 1;
-                    ok = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    bool k = mbar_wait(&p_full[b], (pv >> 1) & 1, abort_flag, lim, SITE_EX_MMA);
+                    k = __all_sync(0xffffffffu, k);
+                    if (!k) return false;
                     tc_fence_after();
                     const uint32_t p_lo = p_lo0 + b * (C::P_BYTES >> 4);
                     auto p_step = [&](int kk) -> uint32_t {
@@ -783,29 +826,56 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                             umma_ts_lh(tmem_o + C::O_BLOCKS * R, tmem + C::ONES_COL, p_step(kk), HI,
                                        IDESC_1, !(first_v && kk == 0));
                     }
-                    for (int s = 0; s < C::KSL && ok; ++s, ++fill) {
-                        const uint32_t slot = fill % C::NS;
-                        ok = mbar_wait(&slot_full[slot], (fill / C::NS) & 1, abort_flag, lim,
-                                       SITE_EX_MMA);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
+#pragma unroll
+                    for (int s = 0; s < C::KSL; ++s) {
+                        const uint32_t f = v_fill + s, slot = f % C::NS;
+                        k = mbar_wait(&slot_full[slot], (f / C::NS) & 1, abort_flag, lim,
+                                      SITE_EX_MMA);
+                        k = __all_sync(0xffffffffu, k);
+                        if (!k) return false;
                         fence_async_smem();
                         tc_fence_after();
                         const uint32_t a0 = v_lo0 + slot * (C::SLOT_BYTES >> 4);
                         if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < EX_BN / 16; ++kk)
-                            umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4), p_step(kk), HI,
-                                       IDESC_O, !(first_v && kk == 0));
-                        umma_commit(&slot_empty[slot]);
+                            for (int kk = 0; kk < EX_BN / 16; ++kk)
+                                umma_ss_lh(tmem_o + s * R, a0 + kk * ((16 * 128) >> 4), p_step(kk),
+                                           HI, IDESC_O, !(first_v && kk == 0));
+                            umma_commit(&slot_empty[slot]);
                         }
                     }
-                    if (!ok) break;
                     if (leader) {
                         umma_commit(&p_empty[b]);
                         if ((lasts >> EX_LAG) & 1) umma_commit(o_full);
                     }
+                    return true;
+                };
+                // Whichever is ready goes first: a unit's last product must not
+                // wait for the next units' keys. (Softmax relies on the order
+                // of different turns only.)
+                const bool has_pv = it >= EX_LAG;
+                bool pv_done = false;
+                if (has_s && has_pv) {
+                    const uint32_t kf = k_fill + C::KSL - 1, vf = v_fill + C::KSL - 1;
+                    const uint64_t t0 = globaltimer_ns();
+                    for (;;) {
+                        if (__all_sync(0xffffffffu,
+                                       mbar_test_wait(&slot_full[kf % C::NS], (kf / C::NS) & 1)))
+                            break;
+                        if (__all_sync(0xffffffffu,
+                                       mbar_test_wait(&p_full[b], (pv >> 1) & 1) &&
+                                           mbar_test_wait(&slot_full[vf % C::NS], (vf / C::NS) & 1))) {
+                            ok = do_pv();
+                            pv_done = true;
+                            break;
+                        }
+                        // (do_s then gives up in the same way)
+                        if (*abort_flag || globaltimer_ns() - t0 > lim) break;
+                    }
                 }
+                if (ok && has_s) ok = do_s();
+                if (ok && has_pv && !pv_done) ok = do_pv();
+                fill = v_fill + (has_pv ? C::KSL : 0);
             }
             if (leader) {
                 umma_commit(drain);
@@ -847,7 +917,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         const float unit_l2 = P.has_cap ? 1.0f : P.scale_l2;
         uint32_t done = 0;  // tiles of the stretch's units before this one
         ExWalk<C::TQ, C::UNIT_COST> W;
-        for (W.seek(P, cum, x0, x1); W.more && ok; W.next_unit(P, cum, x1)) {
+        for (W.start(P, cum, x0, x1); W.more && ok; W.next_unit(P, cum, x1)) {
             const ExUnit& U = W.U;
             const int t_begin = W.begin, t_end = W.end;
             // sums of the weights of pairs of rows (see pair_row), fp32 ones and
