@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_MIN_CTAS) rope_kernel(const
             L = P.cu_k[s + 1] - P.cu_k[s];
         else
             L = P.seq_lens[s];
+        if (P.cu_q == nullptr && L <= 0) return;  // an empty slot of the batch
         pos = L - T + i;
         bool lost;
         row = rope_row<MODE>(P, s, pos, L, lost);

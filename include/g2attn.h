@@ -349,9 +349,10 @@ G2ATTN_API int g2attn_rope(const void* q, const void* k, void* q_out, void* k_ou
  *   k_cache, v_cache (total_k, Hkv, d) packed by cu_seqlens_k (device int32,
  *   num_seqs + 1 entries), whose differences are the L_s.
  *   cu_seqlens_q: device int32, num_seqs + 1 non-decreasing entries from 0 (T_s
- *   may be 0), or NULL when every sequence has exactly one new token (then
- *   total_q must equal num_seqs). Rows of q_out at and behind
- *   cu_seqlens_q[num_seqs] are left as they are.
+ *   may be 0), or NULL when every sequence has one new token (then total_q must
+ *   equal num_seqs, and a sequence of length 0 is an empty slot: its row of
+ *   q_out stays as it is). Rows of q_out at and behind cu_seqlens_q[num_seqs]
+ *   are left as they are.
  *   A token that has no row in its cache (T_s > L_s, lengths past the cache)
  *   writes nothing to it, and g2attn_get_device_error reports
  *   G2ATTN_ERR_CACHE_ROW. Nothing outside the tensors is touched.

@@ -151,6 +151,15 @@ def test_chunks_longer_than_max_T():
         check(out, ro, lse, rl, f"max_T {max_T}")
 
 
+def test_prompt_sized_chunks():
+    """Many units per sequence: prompts of hundreds of tokens in small pages."""
+    out, lse, ro, rl = run([(700, 700), (300, 1500), (1, 900)], 4, 2, 64, 8, 0, 50.0, max_T=700,
+                           seed=21)
+    check(out, ro, lse, rl, "prompts")
+    out, lse, ro, rl = run([(500, 900)], 2, 1, 128, 16, 300, 0.0, seed=22)
+    check(out, ro, lse, rl, "windowed prompt")
+
+
 def test_many_sequences():
     rng = np.random.default_rng(8)
     lens = [(int(t), int(t) + int(s)) for t, s in zip(rng.integers(0, 4, 1024),

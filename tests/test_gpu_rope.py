@@ -249,6 +249,44 @@ def test_tokens_without_a_row_are_dropped_and_reported():
     assert g2.g2attn_get_device_error() == g2.G2ATTN_OK
 
 
+def test_empty_slots_of_a_decode_batch():
+    """One token each, sequences of length 0 among them: no row, no error."""
+    n, H, Hkv, d = 5, 4, 2, 128
+    plan = g2.rope_plan(d)
+    q, k, v = (randn(n, h, d, seed=s).cuda() for s, h in ((1, H), (2, Hkv), (3, Hkv)))
+    lens = torch.tensor([3, 0, 8, 0, 1], dtype=torch.int32).cuda()
+    out = torch.full_like(q, 7.0)
+    kr = torch.zeros(n, 8, Hkv, d, dtype=torch.bfloat16).cuda()
+    vr = kr.clone()
+    g2.rope_append_ring(q, k, v, kr, vr, None, lens, plan, q_out=out)
+    assert (out[[1, 3]] == 7.0).all() and torch.count_nonzero(vr[[1, 3]]) == 0
+    for s, p in ((0, 2), (2, 7), (4, 0)):
+        assert torch.equal(vr[s, p], v[s])
+    want = g2.rope(q, k, (lens - 1).clamp_min(0), plan)
+    assert torch.equal(out[[0, 2, 4]], want[0][[0, 2, 4]])
+    table = torch.tensor([[0, -1], [-1, -1], [1, 2], [-1, -1], [3, -1]], dtype=torch.int32).cuda()
+    kb, vb = torch.zeros(4, 4, Hkv, d, dtype=torch.bfloat16).cuda(), torch.zeros(
+        4, 4, Hkv, d, dtype=torch.bfloat16).cuda()
+    out.fill_(7.0)
+    g2.rope_append_paged(q, k, v, kb, vb, None, table, lens, plan, q_out=out)
+    assert (out[[1, 3]] == 7.0).all() and torch.equal(vb[0, 2], v[0]) and torch.equal(vb[2, 3], v[2])
+    assert torch.equal(kb[3, 0], k[4]) and torch.count_nonzero(vb.abs().amax((-1, -2))) == 3
+    assert g2.g2attn_get_device_error() == g2.G2ATTN_OK
+
+
+def test_single_steps_of_a_dense_batch():
+    """(B, 1, H, d) slices of one projection, as a decode loop has them."""
+    B, H, Hkv, d = 6, 8, 4, 64
+    plan = g2.rope_plan(d, interleaved=True)
+    qkv = randn(B, 1, H + 2 * Hkv, d, seed=8).cuda()
+    pos = torch.tensor([5, 0, 99, 7, 7, 1 << 20], dtype=torch.int32).cuda()
+    got = g2.rope(qkv[:, :, :H], qkv[:, :, H:H + Hkv], pos, plan)
+    want = g2.rope(qkv[:, 0, :H].contiguous(), qkv[:, 0, H:H + Hkv].contiguous(), pos, plan)
+    assert torch.equal(got[0][:, 0], want[0]) and torch.equal(got[1][:, 0], want[1])
+    one = g2.rope(qkv[:1, :, :H], qkv[:1, :, H:H + Hkv], pos[:1], plan)
+    assert torch.equal(one[0], got[0][:1])
+
+
 def test_many_sequences():
     """More sequences than a warp or a CTA has tokens, empty ones among them."""
     n, H, Hkv, d, bs = 3001, 2, 1, 64, 8
