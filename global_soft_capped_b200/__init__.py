@@ -617,7 +617,8 @@ def rope_plan(rotary_dim, *, interleaved=False, device="cuda", frequencies=None,
               **scaling):
     """A :class:`RopePlan` on ``device`` from :func:`rope_frequencies` (whose
     arguments ``scaling`` are) or from ``frequencies`` (radians per position)."""
-    import torch
+    if torch is None:
+        _load_torch()
     m = 1.0
     if frequencies is None:
         frequencies, m = rope_frequencies(rotary_dim, **scaling)
@@ -631,13 +632,25 @@ def rope_plan(rotary_dim, *, interleaved=False, device="cuda", frequencies=None,
     return RopePlan(freqs, int(rotary_dim), bool(interleaved), m if mscale is None else mscale)
 
 
+def _load_torch():
+    """torch for the helpers below, imported with the first of them (a call of
+    these takes a few microseconds, and an import statement in each of the
+    functions it runs through is a good part of that)."""
+    global torch, _raw_stream, _current_device
+    import torch as t
+    _raw_stream, _current_device = t._C._cuda_getCurrentRawStream, t._C._cuda_getDevice
+    torch = t
+
+
+torch = None
+
+
 def _launch(name, device, stream, args):
     """Calls a C entry point with ``args`` and the stream, its device current."""
-    import torch
     index = device.index
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    fn = getattr(load_library(), name)
-    if torch._C._cuda_getDevice() == index:
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or load_library(), name)
+    if _current_device() == index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -649,7 +662,8 @@ def _launch(name, device, stream, args):
 def _heads(name, t, device=None):
     """(token count, heads, d, elements between tokens) of a (..., heads, d)
     bf16 CUDA tensor whose tokens are evenly spaced and whose heads are dense."""
-    import torch
+    if torch is None:
+        _load_torch()
     if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() not in (3, 4):
         raise ValueError(f"{name}: expected a bf16 CUDA tensor (tokens, heads, d) or (B, T, heads, d)")
     if device is not None and t.device != device:
@@ -681,23 +695,22 @@ def _used_on(stream, *tensors):
 def _dense_like(t):
     """A new packed tensor of a shape that :func:`_heads` accepted: evenly spaced
     tokens, for which empty_like's layout is the packed one in the same order."""
-    import torch
     o = torch.empty_like(t)
     return o if o.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _ints(name, t, n, device, dtype=None):
-    import torch
-    if (t.dtype != (dtype or torch.int32) or t.device != device or not t.is_contiguous()
+    if dtype is None:
+        dtype = torch.int32
+    if (t.dtype != dtype or t.device != device or not t.is_contiguous()
             or (n is not None and t.numel() != n)):
-        raise ValueError(f"{name}: expected {'' if n is None else n} contiguous "
-                         f"{dtype or torch.int32} values on {device}")
+        raise ValueError(f"{name}: expected {'' if n is None else n} contiguous {dtype} values "
+                         f"on {device}")
     return t.data_ptr()
 
 
 def _cache(name, t, dims, Hkv, d, device):
     """Pointer of a contiguous bf16 cache (..., Hkv, d)."""
-    import torch
     sh = t.shape
     if (t.dtype != torch.bfloat16 or t.device != device or len(sh) != dims or sh[-1] != d
             or sh[-2] != Hkv or not t.is_contiguous()):
@@ -714,12 +727,10 @@ def _like_cache(name, t, other):
 
 
 def _plan_args(plan, device):
-    import torch
     return _ints("plan.freqs", plan.freqs, plan.rotary_dim // 2, device, torch.int64)
 
 
 def _rope(q, k, positions, plan, inverse, out, stream):
-    import torch
     n, H, d, qs = _heads("q", q)
     nk, Hkv, dk, ks = _heads("k", k, q.device)
     if nk != n or dk != d:
@@ -754,7 +765,6 @@ def rope_backward(dq, dk, positions, plan, *, out=None, stream=None):
 
 def _append(q, k, v, cu_seqlens_q, num_seqs, q_out, stream):
     """Checks common to the appends: (sizes, strides, q_out, cu pointer)."""
-    import torch
     n, H, d, qs = _heads("q", q)
     nk, Hkv, dk, ks = _heads("k", k, q.device)
     nv, Hv, dv, vs = _heads("v", v, q.device)
@@ -826,7 +836,8 @@ def rope_append_paged(q, k, v, k_blocks, v_blocks, cu_seqlens_q, block_table, se
 
 def extend_workspace(max_T, d, device="cuda"):
     """A device buffer of g2attn_extend_workspace_size(max_T, d) bytes."""
-    import torch
+    if torch is None:
+        _load_torch()
     return torch.empty(max(g2attn_extend_workspace_size(max_T, d), 16), dtype=torch.uint8,
                        device=device)
 
@@ -837,7 +848,8 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
     """Attention of short chunks of new tokens, packed q (sum T,H,d), over paged
     caches (num_blocks,bs,Hkv,d) that already hold them; seq_lens with the new
     tokens. Returns (out (sum T,H,d), lse (H, sum T) | None)."""
-    import torch
+    if torch is None:
+        _load_torch()
     if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
         raise ValueError("q: expected a contiguous bf16 CUDA tensor (tokens, H, d)")
     total_q, H, d = q.shape
@@ -873,7 +885,8 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
 
 def pages_workspace(num_seqs, num_blocks, device="cuda"):
     """A device buffer of g2attn_pages_workspace_size(num_seqs, num_blocks) bytes."""
-    import torch
+    if torch is None:
+        _load_torch()
     return torch.empty(max(g2attn_pages_workspace_size(num_seqs, num_blocks), 16),
                        dtype=torch.uint8, device=device)
 
@@ -887,6 +900,8 @@ def _pages_ws(workspace, block_table, num_seqs, num_blocks):
 
 def _table(block_table, ref_counts):
     """(pointer, sequences, columns, pages, counts' pointer) of a page state."""
+    if torch is None:
+        _load_torch()
     if not block_table.is_cuda or block_table.dim() != 2:
         raise ValueError("block_table: expected an int32 CUDA tensor (num_seqs, max_blocks)")
     dev = block_table.device
@@ -931,7 +946,6 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
     """Every sequence s a fork of sequence parents[s] (s: stays). ref_counts in
     place; returns (block_table, seq_lens, copy_src, copy_dst, granted), the
     first two new. Copy the pages (:func:`pages_copy`) before appending."""
-    import torch
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     table = torch.empty_like(block_table)
@@ -948,7 +962,6 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
 def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
     """Renumbers the live pages to the front of the cache, in place; returns
     (copy_src, copy_dst, num_live) for :func:`pages_copy`."""
-    import torch
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     src, dst = block_table.new_empty((2, nb // 2)).unbind(0)
@@ -964,6 +977,8 @@ def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
 def pages_copy(caches, src, dst, *, stream=None):
     """Copies pages src to pages dst in every cache (num_blocks, ...) of a list
     (K and V of all layers), all of one shape and type."""
+    if torch is None:
+        _load_torch()
     caches = list(caches)
     if not caches or caches[0].numel() == 0:
         raise ValueError("caches: expected at least one tensor with pages")
