@@ -564,47 +564,6 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             ok = __all_sync(0xffffffffu, ok);
         };
         const long long rstride = static_cast<long long>(P.Hkv) * D;
-        // Inner tiles (every row visible to some query) of pages of at least 8
-        // rows: one TMA box per page and 64 columns, box e by lane e of the
-        // first warp.
-        const int per_chunk = EX_BN / P.box_rows;
-        const int box_key = (lane % per_chunk) * P.box_rows;  // first row of this lane's box
-        const int box_chunk = lane / per_chunk;
-        struct Tile {
-            int rows[RL];  // this lane's cache rows, -1: not visible
-            int row;       // first cache row of this lane's box
-            int g;         // KV head
-            bool boxes;    // loaded by TMA
-        };
-        auto by_tma = [&](const ExUnit& U, int tile) -> bool {
-            const int k0 = U.base + tile * EX_BN;
-            return P.use_tma != 0 && k0 >= U.lo && k0 + EX_BN <= U.hi;
-        };
-        // Block-table entries of this lane's rows of a key tile, or of its box
-        // (loaded a tile ahead, and only turned into rows when they are needed).
-        auto look_up = [&](const ExUnit& U, int tile, int (&entry)[RL]) {
-            const int* seq = P.table + static_cast<size_t>(U.seq) * P.max_blocks;
-            const int k0 = U.base + tile * EX_BN;
-            if (by_tma(U, tile)) {
-                entry[0] = seq[(k0 + box_key) >> P.block_shift];
-                return;
-            }
-#pragma unroll
-            for (int i = 0; i < RL; ++i) {
-                const int key = k0 + pw * RW + i * 32 + lane;
-                entry[i] = key >= U.lo && key < U.hi ? seq[key >> P.block_shift] : 0;
-            }
-        };
-        // Cache rows of these entries, -1 outside [lo, hi).
-        auto to_rows = [&](const ExUnit& U, int tile, const int (&entry)[RL], int (&rows)[RL]) {
-#pragma unroll
-            for (int i = 0; i < RL; ++i) {
-                const int key = U.base + tile * EX_BN + pw * RW + i * 32 + lane;
-                const int b = max(0, min(entry[i], P.num_blocks - 1));
-                rows[i] = (b << P.block_shift) + (key & ((1 << P.block_shift) - 1));
-                if (key < U.lo || key >= U.hi) rows[i] = -1;
-            }
-        };
         constexpr int LPR = C::SLOT_COLS / 8;  // lanes per row of a slot
         constexpr int RPI = 32 / LPR;          // rows per instruction
         constexpr int PER8 = 8 / RPI;          // instructions per 8 rows (the swizzle's period)
@@ -617,39 +576,98 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             dst8[i] = smem_u32(sSlots) + (piece >> 3) * C::CH_BYTES + (pw * RW + r) * 128 +
                       (((piece & 7) ^ (r & 7)) << 4);
         }
+        // TMA boxes of a tile (pages of at least 8 rows): a page, or 128 rows of
+        // it, by 64 columns; lane b knows the row of box b.
+        const int box_shift = min(P.block_shift, 7);
+        const int per_chunk = EX_BN >> box_shift;
+        const int box = lane & (per_chunk - 1);
+        struct Tile {
+            int rows[RL];  // this lane's cache rows, -1: no query sees them
+            int row;       // first cache row of box lane mod per_chunk
+            int g;         // KV head
+            bool boxes;    // loaded by TMA
+        };
+        // 32 entries of the sequence's table from page `w_page` on, one per lane,
+        // and the 32 after them, loaded long before they are needed: loading a
+        // tile's entries while the tile before it loads left most of their
+        // latency in the producers' way (30,001 keys in pages of 16, d = 256:
+        // 33.3 us against 30.9; 64 sequences of 500 keys, d = 128: 62 against 54).
+        int w_seq = -1, w_page = 0, w_now = 0, w_next = 0;
+        auto entry_of = [&](int seq, int page) -> int {
+            return page < P.max_blocks ? P.table[static_cast<size_t>(seq) * P.max_blocks + page] : 0;
+        };
+        const int tile_pages = max(1, EX_BN >> P.block_shift);
+        auto window = [&](int seq, int page) {  // `page`: a tile's first one
+            if (w_seq == seq && page >= w_page && page + tile_pages <= w_page + 32) return;
+            if (w_seq == seq && page == w_page + 32) {
+                w_now = w_next;
+            } else {
+                w_seq = seq;
+                w_now = entry_of(seq, page + lane);
+            }
+            w_page = page;
+            w_next = entry_of(seq, page + 32 + lane);
+        };
+        auto cache_row = [&](int entry, int key) -> int {
+            return (max(0, min(entry, P.num_blocks - 1)) << P.block_shift) +
+                   (key & ((1 << P.block_shift) - 1));
+        };
+        auto find_tile = [&](const ExUnit& U, int t, Tile& T) {
+            const int k0 = U.base + t * EX_BN;
+            T.g = U.g;
+            T.boxes = P.use_tma != 0 && k0 >= U.lo && k0 + EX_BN <= U.hi;
+            // pages of 1 and 2 rows: more than a window per tile
+            const bool wide = P.block_shift >= 2;
+            const int first = k0 >> P.block_shift;
+            if (wide) window(U.seq, first);
+            if (T.boxes) {
+                const int key = k0 + box * P.box_rows;
+                T.row = cache_row(
+                    __shfl_sync(0xffffffffu, w_now, ((key >> P.block_shift) - w_page) & 31), key);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                const int key = k0 + pw * RW + i * 32 + lane;
+                const bool seen = key >= U.lo && key < U.hi;
+                int e = __shfl_sync(0xffffffffu, w_now, ((key >> P.block_shift) - w_page) & 31);
+                if (!wide) e = seen ? entry_of(U.seq, key >> P.block_shift) : 0;
+                T.rows[i] = seen ? cache_row(e, key) : -1;
+            }
+        };
         auto load_tile = [&](const CUtensorMap* map, const __nv_bfloat16* cache, const Tile& T,
                              int s0) {
             const uint32_t s = fill % C::NS;
             if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
             if (!ok) return;
+            const uint32_t slot = s * C::SLOT_BYTES;
             if (T.boxes) {
                 if (pt == 0) mbar_expect_tx(&slot_full[s], C::SLOT_BYTES);
+                // a 64-column chunk per warp, or every other box: a copy takes its
+                // warp some 90 cycles to issue, 16 of them a slot at pages of 16
+                // (the whole slot by warp 0: 63 instead of 54 us in the case above)
+                const int chunk = C::NCH == 2 ? pw : 0;
+                if (lane < per_chunk && (C::NCH == 2 || (lane & 1) == pw))
+                    tma_load_3d(sSlots + slot + chunk * C::CH_BYTES + (lane << (box_shift + 7)), map,
+                                &slot_full[s], s0 * C::SLOT_COLS + chunk * 64, T.row, T.g);
                 __syncwarp();
-                if (pw == 0 && box_chunk < C::NCH)
-                    tma_load_3d(sSlots + s * C::SLOT_BYTES + box_chunk * C::CH_BYTES + box_key * 128,
-                                map, &slot_full[s], s0 * C::SLOT_COLS + box_chunk * 64, T.row, T.g);
-                cp_async_arrive(&slot_full[s]);
-                ++fill;
-                return;
-            }
-            const int g = T.g;
-            const int (&rows)[RL] = T.rows;
-            const uint32_t slot = s * C::SLOT_BYTES;
-            const __nv_bfloat16* src0 =
-                cache + static_cast<long long>(g) * D + s0 * C::SLOT_COLS + piece * 8;
-            // in batches: the exchanges of a batch overlap (one by one, their
-            // latency was most of a producer's time)
+            } else {
+                const __nv_bfloat16* src0 =
+                    cache + static_cast<long long>(T.g) * D + s0 * C::SLOT_COLS + piece * 8;
+                // in batches: the exchanges of a batch overlap (one by one, their
+                // latency was most of a producer's time)
 #pragma unroll
-            for (int i0 = 0; i0 < RW / RPI; i0 += BATCH) {
-                int row[BATCH];
+                for (int i0 = 0; i0 < RW / RPI; i0 += BATCH) {
+                    int row[BATCH];
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    row[i] = __shfl_sync(0xffffffffu, rows[(i0 + i) * RPI / 32],
-                                         ((i0 + i) * RPI + lane / LPR) & 31);
+                    for (int i = 0; i < BATCH; ++i)
+                        row[i] = __shfl_sync(0xffffffffu, T.rows[(i0 + i) * RPI / 32],
+                                             ((i0 + i) * RPI + lane / LPR) & 31);
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    cp_async16(dst8[(i0 + i) % PER8] + slot + ((i0 + i) / PER8) * 1024,
-                               src0 + max(row[i], 0) * rstride, row[i] >= 0 ? 16 : 0);
+                    for (int i = 0; i < BATCH; ++i)
+                        cp_async16(dst8[(i0 + i) % PER8] + slot + ((i0 + i) / PER8) * 1024,
+                                   src0 + max(row[i], 0) * rstride, row[i] >= 0 ? 16 : 0);
+                }
             }
             cp_async_arrive(&slot_full[s]);  // counts the unit's Q rows in, too
             ++fill;
@@ -672,8 +690,6 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         };
         // K of tile x goes before V of tile x - EX_LAG, the order of their use: V
         // then lands when its weights are ready, and no slot waits for them.
-        // A tile's rows are looked up while the one before it loads.
-        int entry[RL];
         Tile now, past[EX_LAG];
         uint32_t unit = 0;
         ExWalk<C::TQ, C::UNIT_COST> W;
@@ -682,18 +698,10 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             if (W.more) {
                 const ExUnit& U = W.U;
                 if (W.t == W.begin) {
-                    look_up(U, W.t, entry);
                     load_q(U, unit++);
                     if (!ok) break;
                 }
-                now.g = U.g;
-                now.boxes = by_tma(U, W.t);
-                if (now.boxes)
-                    now.row = (max(0, min(entry[0], P.num_blocks - 1)) << P.block_shift) +
-                              ((U.base + W.t * EX_BN + box_key) & ((1 << P.block_shift) - 1));
-                else
-                    to_rows(U, W.t, entry, now.rows);
-                if (W.t + 1 < W.end) look_up(U, W.t + 1, entry);
+                find_tile(U, W.t, now);
                 for (int s = 0; s < C::KSL && ok; ++s) load_tile(&map_k, P.k, now, s);
                 if (++W.t == W.end) W.next_unit(P, cum, x1);
             } else {
