@@ -684,12 +684,25 @@ def _heads(name, t, device=None):
     return n, H, d, step
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here for a call on a stream that is not the current one: their
-    memory is not handed out again before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _new(stream, make, *args, **kwargs):
+    """A tensor for a call on ``stream``, from that stream's memory when one is
+    given: memory of the current stream may still be in use by its earlier work,
+    which the call does not wait for. The current stream, where the result is
+    most likely read, is recorded as a user of it."""
+    if stream is None:
+        return make(*args, **kwargs)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(here)
+    return t
+
+
+def _workspace(t, device):
+    """(pointer, bytes) of a caller's workspace."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _dense_like(t):
@@ -736,8 +749,7 @@ def _rope(q, k, positions, plan, inverse, out, stream):
     if nk != n or dk != d:
         raise ValueError("q and k differ in tokens or head size")
     if out is None:
-        qo, ko = _dense_like(q), _dense_like(k)
-        _used_on(stream, qo, ko)
+        qo, ko = _new(stream, _dense_like, q), _new(stream, _dense_like, k)
         qos, kos = H * d, Hkv * d
     else:
         qo, ko = out
@@ -771,8 +783,7 @@ def _append(q, k, v, cu_seqlens_q, num_seqs, q_out, stream):
     if (nk, dk) != (n, d) or (nv, Hv, dv) != (n, Hkv, d):
         raise ValueError("q, k and v differ in tokens, heads or head size")
     if q_out is None:
-        q_out = _dense_like(q)
-        _used_on(stream, q_out)
+        q_out = _new(stream, _dense_like, q)
     elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.dtype != q.dtype \
             or q_out.device != q.device:
         raise ValueError("q_out: expected a contiguous bf16 tensor like q")
@@ -859,27 +870,25 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: expected one row per sequence")
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        out = _new(stream, torch.empty_like, q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
             or not out.is_contiguous():
         raise ValueError("out: expected a contiguous bf16 tensor like q")
     if lse is None and want_lse:
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
-        _used_on(stream, lse)
+        lse = _new(stream, torch.empty, (H, total_q), dtype=torch.float32, device=q.device)
     elif lse is not None and (lse.shape != (H, total_q) or lse.dtype != torch.float32
                               or lse.device != q.device or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous fp32 tensor (H, tokens)")
     if workspace is None:
-        workspace = extend_workspace(max_T, d, q.device)
-        _used_on(stream, workspace)
+        workspace = _new(stream, extend_workspace, max_T, d, q.device)
+    ws, ws_bytes = _workspace(workspace, q.device)
     _launch("g2attn_extend_paged", q.device, stream, (
         q.data_ptr(), kc, vc, out.data_ptr(), None if lse is None else lse.data_ptr(),
         _ints("cu_seqlens_q", cu_seqlens_q, n + 1, q.device),
         _ints("block_table", block_table, None, q.device),
         _ints("seq_lens", seq_lens, None, q.device), n, total_q, k_blocks.shape[0],
         k_blocks.shape[1], block_table.shape[1], int(max_T), H, k_blocks.shape[2], d, query_scale,
-        softcap, int(window), workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        softcap, int(window), ws, ws_bytes))
     return out, lse
 
 
@@ -891,11 +900,12 @@ def pages_workspace(num_seqs, num_blocks, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
-def _pages_ws(workspace, block_table, num_seqs, num_blocks):
-    if workspace is not None:
-        return workspace
-    n = load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
-    return block_table.new_empty((n + 3) // 4)
+def _pages_ws(workspace, stream, block_table, num_seqs, num_blocks):
+    """The workspace (kept alive by the caller), its pointer and bytes."""
+    if workspace is None:
+        n = load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
+        workspace = _new(stream, block_table.new_empty, (n + 3) // 4)
+    return workspace, *_workspace(workspace, block_table.device)
 
 
 def _table(block_table, ref_counts):
@@ -918,17 +928,16 @@ def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, copies=Fal
     :func:`pages_copy`, without it such a sequence is refused."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    ws = _pages_ws(workspace, block_table, n, nb)
+    ws, wp, wb = _pages_ws(workspace, stream, block_table, n, nb)
     src = dst = None
     if copies:
-        granted, src, dst = block_table.new_empty((3, n)).unbind(0)
+        granted, src, dst = _new(stream, block_table.new_empty, (3, n)).unbind(0)
     else:
-        granted = block_table.new_empty(n)
-    _used_on(stream, granted, ws)
+        granted = _new(stream, block_table.new_empty, n)
     _launch("g2attn_pages_grow", dev, stream, (
         tp, _ints("seq_lens", seq_lens, n, dev), rp, _ints("add", add, n, dev), granted.data_ptr(),
         None if src is None else src.data_ptr(), None if dst is None else dst.data_ptr(), n, nb,
-        int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
+        int(block_size), cols, wp, wb))
     return (granted, src, dst) if copies else granted
 
 
@@ -948,14 +957,13 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
     first two new. Copy the pages (:func:`pages_copy`) before appending."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    table = torch.empty_like(block_table)
-    lens, src, dst, granted = block_table.new_empty((4, n)).unbind(0)
-    ws = _pages_ws(workspace, block_table, n, nb)
-    _used_on(stream, table, lens, ws)
+    table = _new(stream, torch.empty_like, block_table)
+    lens, src, dst, granted = _new(stream, block_table.new_empty, (4, n)).unbind(0)
+    ws, wp, wb = _pages_ws(workspace, stream, block_table, n, nb)
     _launch("g2attn_pages_fork", dev, stream, (
         tp, _ints("seq_lens", seq_lens, n, dev), _ints("parents", parents, n, dev),
         table.data_ptr(), lens.data_ptr(), rp, src.data_ptr(), dst.data_ptr(), granted.data_ptr(),
-        n, nb, int(block_size), cols, ws.data_ptr(), ws.numel() * ws.element_size()))
+        n, nb, int(block_size), cols, wp, wb))
     return table, lens, src, dst, granted
 
 
@@ -964,13 +972,11 @@ def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
     (copy_src, copy_dst, num_live) for :func:`pages_copy`."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
-    src, dst = block_table.new_empty((2, nb // 2)).unbind(0)
-    live = block_table.new_empty(1)
-    ws = _pages_ws(workspace, block_table, n, nb)
-    _used_on(stream, src, live, ws)
+    src, dst = _new(stream, block_table.new_empty, (2, nb // 2)).unbind(0)
+    live = _new(stream, block_table.new_empty, 1)
+    ws, wp, wb = _pages_ws(workspace, stream, block_table, n, nb)
     _launch("g2attn_pages_compact", dev, stream, (
-        tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, ws.data_ptr(),
-        ws.numel() * ws.element_size()))
+        tp, rp, src.data_ptr(), dst.data_ptr(), live.data_ptr(), n, nb, cols, wp, wb))
     return src, dst, live
 
 

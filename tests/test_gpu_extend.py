@@ -339,3 +339,44 @@ def test_helper_checks():
     with pytest.raises(g2.G2AttnError):
         g2.extend_paged(q, kb, vb, cu, table, lens, T, workspace=torch.empty(16, dtype=torch.uint8,
                                                                             device="cuda"))
+
+
+def test_results_for_another_stream_are_not_memory_still_in_use():
+    """A block that the current stream freed, and that its queued work still
+    writes, must not become the result of a call on another stream."""
+    args, _ = _inputs([(5, 300), (2, 64)], 8, 4, 256, 16)
+    plan = g2.rope_plan(256)
+    pos = torch.arange(7, dtype=torch.int32).cuda()
+    k = torch.randn(7, 4, 256).bfloat16().cuda()
+    parents = torch.tensor([1, 0], dtype=torch.int32).cuda()
+    refs = torch.zeros(args[1].shape[0], dtype=torch.int32).cuda()
+    refs[args[4][args[4] >= 0].long()] = 1
+    calls = [lambda st: g2.extend_paged(*args, query_scale=0.1, stream=st),
+             lambda st: g2.rope(args[0], k, pos, plan, stream=st),
+             lambda st: g2.pages_fork(args[4], args[5], counts.pop(), parents, 16, stream=st)]
+    counts = [refs.clone(), refs.clone()]  # (a fork changes them)
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        held = [torch.empty_like(t) for t in want for _ in range(3)]
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        for t in held:
+            t.fill_(7)
+        del held, t
+        got = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_workspaces_elsewhere_are_refused():
+    args, _ = _inputs([(2, 30)], 4, 2, 128, 16)
+    n = g2.g2attn_extend_workspace_size(8, 128)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(n, 2, dtype=torch.uint8).cuda()[:, 0]):
+        with pytest.raises(ValueError):
+            g2.extend_paged(*args, workspace=ws)
+    table = torch.full((2, 4), -1, dtype=torch.int32).cuda()
+    zero = torch.zeros(8, dtype=torch.int32).cuda()
+    with pytest.raises(ValueError):
+        g2.pages_grow(table, zero[:2], zero, zero[:2], 16, workspace=torch.empty(4096))
