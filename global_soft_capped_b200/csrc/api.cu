@@ -634,6 +634,17 @@ size_t extend_ws_bytes(int max_T, int d) {
            (sizeof(int4) + extend_rows(max_T) * (static_cast<size_t>(d) + 4) * sizeof(float));
 }
 
+// Whether the launch's tiles can be numbered in 31 bits whatever the lengths
+// are: the most units times the most tiles that the shapes allow.
+bool extend_tiles_fit(int num_seqs, int total_q, long long table_rows, int max_T, int Hkv, int d,
+                      int window) {
+    const long long tq = extend_rows(max_T) / 2;
+    const long long units = (total_q / tq + num_seqs) * Hkv;
+    const long long keys = window > 0 ? std::min(table_rows, window + tq) : table_rows;
+    const long long places = keys / g2::EX_BN + 2 + g2::ex_unit_cost(d);
+    return units <= g2::EX_MAX_TILES / places;
+}
+
 template <int D, int R, int SM>
 int launch_extend(g2::ExParams& P, cudaStream_t stream) {
     using C = g2::ExCfg<D, R>;
@@ -1186,6 +1197,9 @@ int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_block
     // (a tile's end may lie one tile past the last key)
     if (static_cast<long long>(num_blocks) * block_size > INT32_MAX ||
         static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX - 2 * g2::EX_BN)
+        return G2ATTN_ERR_UNSUPPORTED;
+    if (!extend_tiles_fit(num_seqs, total_q, static_cast<long long>(max_blocks_per_seq) * block_size,
+                          max_T, Hkv, d, window))
         return G2ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k_blocks) || !aligned16(v_blocks) || !aligned16(out) ||
         (lse && !aligned16(lse)) || !aligned4(cu_seqlens_q) || !aligned4(block_table) ||

@@ -64,19 +64,21 @@ constexpr int EX_LAG = EX_S_BUFS - 1; // tiles by which V and its product follow
 constexpr int EX_MAX_SLOTS = 12;      // ring slots, whatever fits
 constexpr int EX_MAX_SEQS = 1024;     // per-launch table in shared memory
 constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
-// Tiles a launch numbers at most (2^38 keys over all heads: days of work; the
-// queries of tiles past it are not answered).
+// Places that a launch's line has at most: calls whose shapes allow for more are
+// refused (malformed offsets can still make more; those are cut off).
 constexpr long long EX_MAX_TILES = 0x7fffffffll;
 constexpr float EX_RAISE_LOG2 = 64.0f;   // see the softmax above
 constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key yet
 
+// Places in the line of tiles that a unit takes besides its tiles: what its
+// start and end cost, in tiles (chunks of up to 32 tokens of 24 ragged
+// sequences, d = 128: 288 us without, 259 with 2, 238 with 4, 235 with 6)
+constexpr int ex_unit_cost(int d) { return 768 / d; }
+
 template <int D, int R>
 struct ExCfg {
     static constexpr int TQ = R / 2;                      // positions per unit
-    // Places in the line of tiles that a unit takes besides its tiles: what its
-    // start and end cost, in tiles (chunks of up to 32 tokens of 24 ragged
-    // sequences, d = 128: 288 us without, 259 with 2, 238 with 4, 235 with 6)
-    static constexpr int UNIT_COST = 768 / D;
+    static constexpr int UNIT_COST = ex_unit_cost(D);
     static constexpr int NWG = R == 64 ? 4 : 2;           // softmax warpgroups
     static constexpr int HC = R / NWG;                    // rows per softmax warpgroup
     static constexpr int SM_WARPS = 4 * NWG;

@@ -422,7 +422,12 @@ G2ATTN_API size_t g2attn_extend_workspace_size(int max_T, int d);
  *   workspace: at least g2attn_extend_workspace_size(max_T, d) bytes, 16-byte
  *   aligned, no initial contents needed. Calls that may run at the same time
  *   (two streams, two graphs) need workspaces of their own.
- * Limits: num_seqs <= 1024 (as g2attn_prefill_varlen). Two kernels on `stream`.
+ *   As in the other calls with matrix products, an infinite or NaN value row
+ *   that some query of a chunk sees can reach the chunk's other queries.
+ * Limits: num_seqs <= 1024 (as g2attn_prefill_varlen), and the 128-key tiles of
+ * all units together, for sequences as long as the table's rows, fit 31 bits
+ * (1,024 sequences of 8 tokens and 16 KV heads: 8 million keys each; a max_T far
+ * below chunks of many thousand tokens makes more units). Two kernels on `stream`.
  */
 G2ATTN_API int g2attn_extend_paged(const void* q, const void* k_blocks, const void* v_blocks,
                         void* out, float* lse, const int* cu_seqlens_q, const int* block_table,

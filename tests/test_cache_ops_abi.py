@@ -255,3 +255,16 @@ def test_helpers_refuse_host_tensors():
     with pytest.raises(ValueError):
         g2.pages_truncate(torch.zeros(2, 2, dtype=torch.int32), None,
                           torch.zeros(2, dtype=torch.int32), None, 16)
+
+
+def test_extend_refuses_more_tiles_than_it_can_number():
+    """A million tokens over as many keys in units of 8 positions (max_T 4) would be
+    4 * 131,073 * 8,200 tiles; in units of 32 they fit, and the next check speaks."""
+    big = dict(total_q=1 << 20, num_seqs=1, max_blocks_per_seq=1 << 16, workspace=None)
+    assert call(g2.g2attn_extend_paged, EXTEND, big) == UNSUPPORTED
+    assert call(g2.g2attn_extend_paged, EXTEND, {**big, "max_T": 1 << 20}) == WORKSPACE
+    assert call(g2.g2attn_extend_paged, EXTEND, {**big, "window": 4096}) == WORKSPACE
+    wide = dict(total_q=8192, num_seqs=1024, Hkv=16, H=32, max_blocks_per_seq=1 << 20)
+    assert call(g2.g2attn_extend_paged, EXTEND, {**wide, "workspace": None}) == UNSUPPORTED
+    wide["max_blocks_per_seq"] = 500_000  # 8,000,000 keys
+    assert call(g2.g2attn_extend_paged, EXTEND, {**wide, "workspace": None}) == WORKSPACE
