@@ -166,7 +166,8 @@ __device__ __forceinline__ int ex_len(const ExParams& P, int s) {
 // positions p0 .. p0 + n - 1 of a sequence of length L. Tile 0 starts at the box
 // that holds the first visible key.
 __device__ __forceinline__ int ex_range(const ExParams& P, int p0, int n, int L, int& lo, int& hi) {
-    lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+    // (compared first: p0 - window wraps round for the largest windows and p0 < 0)
+    lo = P.window > 0 && p0 >= P.window ? p0 - P.window + 1 : 0;
     hi = min(max(0, p0 + n), L);
     return max(1, (hi - (lo & -P.box_rows) + EX_BN - 1) / EX_BN);
 }

@@ -230,6 +230,19 @@ def test_rows_without_keys():
     assert torch.count_nonzero(out) == 0 and (lse == float("-inf")).all()
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_largest_windows(window):
+    """A window past every position changes nothing, also where the first
+    queries sit before the first key and their position less the window wraps round."""
+    args, _ = _inputs([(12, 12), (3, 300)], 4, 2, 64, 8)
+    lens = torch.tensor([2, 300], dtype=torch.int32).cuda()
+    for cap in (50.0, 0.0):
+        out, lse = g2.extend_paged(*args[:5], lens, 12, query_scale=0.1, softcap=cap, window=window)
+        ro, rl = g2.extend_paged(*args[:5], lens, 12, query_scale=0.1, softcap=cap)
+        assert torch.isfinite(rl[:, 10:]).all() and (rl[:, :10] == float("-inf")).all()
+        assert torch.equal(out, ro) and torch.equal(lse, rl)
+
+
 def test_malformed_tables_stay_in_bounds():
     """Entries outside the cache, lengths past the table, offsets past the
     tensors: undefined results, but finite ones, as every row read is a row of
