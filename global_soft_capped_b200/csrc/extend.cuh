@@ -31,12 +31,14 @@
 //                key; writes P as bf16 into shared memory; at a unit's end
 //                reads O^T (lane = d column) and writes out or the partial.
 //   1 warp       tensor memory, one thread issues the UMMAs.
-//   2 producers  K and V into a ring of 128-byte-swizzled tiles. Tiles whose rows
-//                all count come by TMA, a box per page; the others (a sequence's
-//                end, a window's start, pages under 8 rows) and Q by 16-byte
-//                asynchronous copies of rows looked up one by one, with zeros
-//                for rows that no query sees (what the cache holds there, NaN
-//                included, does not matter).
+//   2 producers  K and V into a ring of 128-byte-swizzled tiles, by TMA, a box per
+//                page; a box that no query sees is read from outside the cache, as
+//                zeros. Boxes seen in part (a sequence's end, a window's
+//                start), pages under 8 rows and Q come by 16-byte asynchronous
+//                copies, with zeros for rows that no query sees (what the cache
+//                holds there, NaN included, does not matter). Whole tiles by such
+//                copies wherever one row was not seen: 64 sequences of 64 keys, d = 128,
+//                pages of 16: 29.7 us against 22.3; of 150 keys and 32 tokens: 69 against 60.
 //   1 warp       writes the CTA's merge record.
 // Softmax: fp32, log2 domain. With the cap the prefill's fixed shift where it
 // fits. Else a reference per row that is the row's maximum over its first tile
@@ -585,11 +587,13 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         const int per_chunk = EX_BN >> box_shift;
         const int box = lane & (per_chunk - 1);
         struct Tile {
-            int rows[RL];  // this lane's cache rows, -1: no query sees them
+            int rows[RL];  // pages under 8 rows: this lane's cache rows, -1: no query
+                           // sees them; else the tile's rows [first, end) that are seen
             int row;       // first cache row of box lane mod per_chunk
             int g;         // KV head
-            bool boxes;    // loaded by TMA
+            uint32_t parts;  // boxes that are seen in part (bits)
         };
+        static_assert(RL == 2, "rows or the seen range");
         // 32 entries of the sequence's table from page `w_page` on, one per lane,
         // and the 32 after them, loaded long before they are needed: loading a
         // tile's entries while the tile before it loads left most of their
@@ -615,18 +619,25 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             return (max(0, min(entry, P.num_blocks - 1)) << P.block_shift) +
                    (key & ((1 << P.block_shift) - 1));
         };
+        // Boxes that queries see whole come by TMA, and so do those that none
+        // sees, from rows outside the cache, as zeros.
         auto find_tile = [&](const ExUnit& U, int t, Tile& T) {
             const int k0 = U.base + t * EX_BN;
             T.g = U.g;
-            T.boxes = P.use_tma != 0 && k0 >= U.lo && k0 + EX_BN <= U.hi;
+            T.parts = 0;
             // pages of 1 and 2 rows: more than a window per tile
             const bool wide = P.block_shift >= 2;
-            const int first = k0 >> P.block_shift;
-            if (wide) window(U.seq, first);
-            if (T.boxes) {
-                const int key = k0 + box * P.box_rows;
-                T.row = cache_row(
-                    __shfl_sync(0xffffffffu, w_now, ((key >> P.block_shift) - w_page) & 31), key);
+            if (wide) window(U.seq, k0 >> P.block_shift);
+            if (P.use_tma != 0) {
+                const int key = k0 + box * P.box_rows, end = key + P.box_rows;
+                const int e =
+                    __shfl_sync(0xffffffffu, w_now, ((key >> P.block_shift) - w_page) & 31);
+                const bool none = end <= U.lo || key >= U.hi;
+                const bool part = !none && (key < U.lo || end > U.hi);
+                T.row = none ? -EX_BN : cache_row(e, key);
+                T.parts = __ballot_sync(0xffffffffu, part && lane < per_chunk);
+                T.rows[0] = U.lo - k0;
+                T.rows[1] = U.hi - k0;
                 return;
             }
 #pragma unroll
@@ -644,19 +655,38 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
             if (fill >= static_cast<uint32_t>(C::NS)) await(&slot_empty[s], ((fill / C::NS) - 1) & 1);
             if (!ok) return;
             const uint32_t slot = s * C::SLOT_BYTES;
-            if (T.boxes) {
-                if (pt == 0) mbar_expect_tx(&slot_full[s], C::SLOT_BYTES);
+            const __nv_bfloat16* src0 =
+                cache + static_cast<long long>(T.g) * D + s0 * C::SLOT_COLS + piece * 8;
+            if (P.use_tma != 0) {
+                if (pt == 0)
+                    mbar_expect_tx(&slot_full[s], C::SLOT_BYTES - __popc(T.parts) * P.box_rows *
+                                                                      (C::SLOT_COLS * 2));
                 // a 64-column chunk per warp, or every other box: a copy takes its
                 // warp some 90 cycles to issue, 16 of them a slot at pages of 16
                 // (the whole slot by warp 0: 63 instead of 54 us in the case above)
                 const int chunk = C::NCH == 2 ? pw : 0;
-                if (lane < per_chunk && (C::NCH == 2 || (lane & 1) == pw))
+                if (lane < per_chunk && ((T.parts >> lane) & 1) == 0 &&
+                    (C::NCH == 2 || (lane & 1) == pw))
                     tma_load_3d(sSlots + slot + chunk * C::CH_BYTES + (lane << (box_shift + 7)), map,
                                 &slot_full[s], s0 * C::SLOT_COLS + chunk * 64, T.row, T.g);
                 __syncwarp();
+                // the boxes at the ends of what is seen (one or two): the warps take
+                // groups of 8 of their rows in turn
+                for (uint32_t m = T.parts; m != 0; m &= m - 1) {
+                    const int b = __ffs(m) - 1;
+                    const int r0 = b << box_shift;  // the box's first row of the tile
+                    const int row0 = __shfl_sync(0xffffffffu, T.row, b);
+                    for (int j = pw * 8; j < P.box_rows; j += EX_PROD_WARPS * 8) {
+#pragma unroll
+                        for (int i = 0; i < PER8; ++i) {
+                            const int in = j + i * RPI + lane / LPR, r = r0 + in;
+                            const bool seen = r >= T.rows[0] && r < T.rows[1];
+                            cp_async16(dst8[i] + slot + (r0 + j - pw * RW) * 128,
+                                       src0 + (seen ? row0 + in : 0) * rstride, seen ? 16 : 0);
+                        }
+                    }
+                }
             } else {
-                const __nv_bfloat16* src0 =
-                    cache + static_cast<long long>(T.g) * D + s0 * C::SLOT_COLS + piece * 8;
                 // in batches: the exchanges of a batch overlap (one by one, their
                 // latency was most of a producer's time)
 #pragma unroll
@@ -861,9 +891,9 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                     }
                     return true;
                 };
-                // Whichever is ready goes first: a unit's last product must not
-                // wait for the next units' keys. (Softmax relies on the order
-                // of different turns only.)
+                // Whichever is ready goes first, the product if both are: a unit's
+                // end waits for it, while the scores are two tiles ahead. (Softmax
+                // relies on the order of different turns only.)
                 const bool has_pv = it >= EX_LAG;
                 bool pv_done = false;
                 if (has_s && has_pv) {
@@ -871,15 +901,15 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                     const uint64_t t0 = globaltimer_ns();
                     for (;;) {
                         if (__all_sync(0xffffffffu,
-                                       mbar_test_wait(&slot_full[kf % C::NS], (kf / C::NS) & 1)))
-                            break;
-                        if (__all_sync(0xffffffffu,
                                        mbar_test_wait(&p_full[b], (pv >> 1) & 1) &&
                                            mbar_test_wait(&slot_full[vf % C::NS], (vf / C::NS) & 1))) {
                             ok = do_pv();
                             pv_done = true;
                             break;
                         }
+                        if (__all_sync(0xffffffffu,
+                                       mbar_test_wait(&slot_full[kf % C::NS], (kf / C::NS) & 1)))
+                            break;
                         // (do_s then gives up in the same way)
                         if (*abort_flag || globaltimer_ns() - t0 > lim) break;
                     }
@@ -1175,16 +1205,25 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 ex_tmem_ld<HC>(o_addr + C::O_BLOCKS * R, lsum);
             } else {
 #pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    lsum[c] = 0.f;
+                for (int c = 0; c < HC; c += 4) {
+                    float4 l = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) lsum[c] += ssum[(w * NSUM + 1) * HC + c];
+                    for (int w = 0; w < 4; ++w) {
+                        const float4 x =
+                            *reinterpret_cast<const float4*>(ssum + (w * NSUM + 1) * HC + c);
+                        l = make_float4(l.x + x.x, l.y + x.y, l.z + x.z, l.w + x.w);
+                    }
+                    lsum[c] = l.x;
+                    lsum[c + 1] = l.y;
+                    lsum[c + 2] = l.z;
+                    lsum[c + 3] = l.w;
                 }
             }
             const bool whole = t_begin == 0 && t_end == U.tiles;
             // a stretch's first segment has slot 0, its last one slot 1
             const size_t ws = static_cast<size_t>(blockIdx.x) * 2 + (unit == 0 ? 0 : 1);
             const int rows = 2 * U.tvalid;
+            const long long pair = static_cast<long long>(P.H) * D;  // the two heads of a position
             __nv_bfloat16* out0 = P.out + (static_cast<size_t>(U.qrow) * P.H + 2 * U.g) * D;
 #pragma unroll
             for (int o = 0; o < C::O_BLOCKS; ++o) {
@@ -1192,15 +1231,21 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 ex_tmem_ld<HC>(o_addr + o * R, a);
                 const int dcol = o * 128 + key_l;
                 if (D < 128 && key_l >= D) continue;
+                if (whole) {
+                    __nv_bfloat16* to = out0 + (wg * HC / 2) * pair + dcol;
 #pragma unroll
-                for (int c = 0; c < HC; ++c) {
-                    const int r = wg * HC + c;
-                    if (r >= rows) continue;
-                    if (whole)
-                        out0[(static_cast<size_t>(r >> 1) * P.H + (r & 1)) * D + dcol] =
-                            __float2bfloat16_rn(lsum[c] > 0.f ? a[c] * rcp_approx(lsum[c]) : 0.f);
-                    else
-                        P.ws_o[(ws * R + r) * D + dcol] = a[c];
+                    for (int c = 0; c < HC; c += 2, to += pair) {
+                        if (wg * HC + c >= rows) break;  // (rows is even)
+                        to[0] = __float2bfloat16_rn(
+                            lsum[c] > 0.f ? a[c] * rcp_approx(lsum[c]) : 0.f);
+                        to[D] = __float2bfloat16_rn(
+                            lsum[c + 1] > 0.f ? a[c + 1] * rcp_approx(lsum[c + 1]) : 0.f);
+                    }
+                } else {
+                    float* to = P.ws_o + (ws * R + wg * HC) * D + dcol;
+#pragma unroll
+                    for (int c = 0; c < HC; ++c)
+                        if (wg * HC + c < rows) to[c * D] = a[c];
                 }
             }
             if (key_l < HC && wg * HC + key_l < rows) {
