@@ -27,6 +27,7 @@ first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -845,6 +846,17 @@ def rope_append_paged(q, k, v, k_blocks, v_blocks, cu_seqlens_q, block_table, se
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
+def _extend_bytes(max_T, d):
+    """Workspace bytes; a size function, so the call (a microsecond) is made once."""
+    return load_library().g2attn_extend_workspace_size(max_T, d)
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_bytes(num_seqs, num_blocks):
+    return load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
+
+
 def extend_workspace(max_T, d, device="cuda"):
     """A device buffer of g2attn_extend_workspace_size(max_T, d) bytes."""
     if torch is None:
@@ -864,6 +876,7 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
     if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
         raise ValueError("q: expected a contiguous bf16 CUDA tensor (tokens, H, d)")
     total_q, H, d = q.shape
+    max_T = int(max_T)
     kc = _cache("k_blocks", k_blocks, 4, k_blocks.shape[-2], d, q.device)
     vc = _like_cache("v_blocks", v_blocks, k_blocks)
     n = seq_lens.numel()
@@ -875,19 +888,19 @@ def extend_paged(q, k_blocks, v_blocks, cu_seqlens_q, block_table, seq_lens, max
             or not out.is_contiguous():
         raise ValueError("out: expected a contiguous bf16 tensor like q")
     if lse is None and want_lse:
-        lse = _new(stream, torch.empty, (H, total_q), dtype=torch.float32, device=q.device)
+        lse = _new(stream, q.new_empty, (H, total_q), dtype=torch.float32)
     elif lse is not None and (lse.shape != (H, total_q) or lse.dtype != torch.float32
                               or lse.device != q.device or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous fp32 tensor (H, tokens)")
     if workspace is None:
-        workspace = _new(stream, extend_workspace, max_T, d, q.device)
+        workspace = _new(stream, q.new_empty, _extend_bytes(max_T, d), dtype=torch.uint8)
     ws, ws_bytes = _workspace(workspace, q.device)
     _launch("g2attn_extend_paged", q.device, stream, (
         q.data_ptr(), kc, vc, out.data_ptr(), None if lse is None else lse.data_ptr(),
         _ints("cu_seqlens_q", cu_seqlens_q, n + 1, q.device),
         _ints("block_table", block_table, None, q.device),
         _ints("seq_lens", seq_lens, None, q.device), n, total_q, k_blocks.shape[0],
-        k_blocks.shape[1], block_table.shape[1], int(max_T), H, k_blocks.shape[2], d, query_scale,
+        k_blocks.shape[1], block_table.shape[1], max_T, H, k_blocks.shape[2], d, query_scale,
         softcap, int(window), ws, ws_bytes))
     return out, lse
 
@@ -903,8 +916,8 @@ def pages_workspace(num_seqs, num_blocks, device="cuda"):
 def _pages_ws(workspace, stream, block_table, num_seqs, num_blocks):
     """The workspace (kept alive by the caller), its pointer and bytes."""
     if workspace is None:
-        n = load_library().g2attn_pages_workspace_size(num_seqs, num_blocks)
-        workspace = _new(stream, block_table.new_empty, (n + 3) // 4)
+        workspace = _new(stream, block_table.new_empty,
+                         (_pages_bytes(num_seqs, num_blocks) + 3) // 4)
     return workspace, *_workspace(workspace, block_table.device)
 
 
