@@ -243,6 +243,17 @@ def test_largest_windows(window):
         assert torch.equal(out, ro) and torch.equal(lse, rl)
 
 
+@pytest.mark.parametrize("bs", [4, 8, 16, 64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pages_seen_in_part(bs, d):
+    """What is seen starts and ends inside pages, one and the same among them,
+    and ends at their borders: whole, partly seen and unseen pages side by side."""
+    lens = [(3, 70), (1, 64), (2, 129), (1, 7), (4, 260), (2, 384), (20, 140)]
+    for window, cap in ((0, 50.0), (5, 50.0), (70, 0.0)):
+        out, lse, ro, rl = run(lens, 4, 2, d, bs, window, cap, seed=bs + d)
+        check(out, ro, lse, rl, f"pages of {bs}, d {d}, window {window}")
+
+
 def test_malformed_tables_stay_in_bounds():
     """Entries outside the cache, lengths past the table, offsets past the
     tensors: undefined results, but finite ones, as every row read is a row of
