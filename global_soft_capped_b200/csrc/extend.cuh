@@ -1243,10 +1243,13 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
 #pragma unroll
                     for (int c = 0; c < HC; c += 2, to += pair) {
                         if (wg * HC + c >= rows) break;  // (rows is even)
-                        to[0] = __float2bfloat16_rn(
-                            lsum[c] > 0.f ? a[c] * rcp_approx(lsum[c]) : 0.f);
-                        to[D] = __float2bfloat16_rn(
-                            lsum[c + 1] > 0.f ? a[c + 1] * rcp_approx(lsum[c + 1]) : 0.f);
+                        // A query before the first key sees none, every other one
+                        // its own position: the sums do not decide that, as those
+                        // of a NaN must stay NaN.
+                        const bool sees = U.p0 + ((wg * HC + c) >> 1) >= 0;
+                        to[0] = __float2bfloat16_rn(sees ? a[c] * rcp_approx(lsum[c]) : 0.f);
+                        to[D] =
+                            __float2bfloat16_rn(sees ? a[c + 1] * rcp_approx(lsum[c + 1]) : 0.f);
                     }
                 } else {
                     float* to = P.ws_o + (ws * R + wg * HC) * D + dcol;
@@ -1271,7 +1274,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                     s[2] = l;
                 } else if (P.lse != nullptr) {
                     P.lse[static_cast<size_t>(2 * U.g + (r & 1)) * P.total_q + U.qrow + (r >> 1)] =
-                        a > 0.f ? (mm + log2f(a)) * 0.69314718055994531f : -INFINITY;
+                        U.p0 + (r >> 1) >= 0 ? (mm + log2f(a)) * 0.69314718055994531f : -INFINITY;
                 }
             }
             tc_fence_before();
@@ -1380,7 +1383,9 @@ __global__ void __launch_bounds__(256) extend_merge(const ExParams P) {
             __syncwarp();  // w is written anew for the next row
         }
         if (!on || member != 0) continue;
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        // (a unit with a query before the first key has one tile: none is cut, and
+        // every row here sees a key)
+        const float inv = 1.0f / l;
         const int qrow = qrow0 + (r >> 1), h = 2 * g + (r & 1);
         uint32_t* dst = reinterpret_cast<uint32_t*>(
             P.out + (static_cast<size_t>(qrow) * P.H + h) * D + col);
@@ -1389,7 +1394,7 @@ __global__ void __launch_bounds__(256) extend_merge(const ExParams P) {
             dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
         if (e % BLK == 0 && lane == 0 && P.lse != nullptr)
             P.lse[static_cast<size_t>(h) * P.total_q + qrow] =
-                a > 0.f ? (M + log2f(a)) * 0.69314718055994531f : -INFINITY;
+                (M + log2f(a)) * 0.69314718055994531f;
     }
 }
 

@@ -415,7 +415,9 @@ G2ATTN_API size_t g2attn_extend_workspace_size(int max_T, int d);
  *   append them first) as g2attn_decode_paged. Rows of pages beyond L_s are
  *   not read. Table entries outside [0, num_blocks) are clamped; malformed
  *   lengths or tables give undefined results, never an out-of-bounds access.
- *   A query that sees no key (T_s > L_s) gets out = 0 and lse = -inf.
+ *   A query that sees no key (T_s > L_s) gets out = 0 and lse = -inf. A NaN in a
+ *   query or in a key that it sees, or without the cap a score that overflows,
+ *   makes its row NaN, as in the other calls.
  *   max_T: the longest chunk the caller expects; it picks the kernel's row count
  *   (16, 32 or 64 rows for chunks of up to 8, 16 or more positions) and the
  *   workspace. Longer chunks than max_T are still right.
