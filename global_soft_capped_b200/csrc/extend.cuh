@@ -917,8 +917,11 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                             pv_done = true;
                             break;
                         }
-                        // (do_s then gives up in the same way)
-                        if (*abort_flag || globaltimer_ns() - t0 > lim) break;
+                        // (do_s then gives up in the same way; voted, as each lane
+                        // has its own timer and all must leave together)
+                        if (__any_sync(0xffffffffu,
+                                       *abort_flag != 0 || globaltimer_ns() - t0 > lim))
+                            break;
                     }
                 }
                 if (ok && has_s) ok = do_s();
