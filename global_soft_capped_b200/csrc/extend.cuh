@@ -42,9 +42,10 @@
 //   1 warp       writes the CTA's merge record.
 // Softmax: fp32, log2 domain. With the cap the prefill's fixed shift where it
 // fits. Else a reference per row that is the row's maximum over its first tile
-// and is only raised (and O and the sums rescaled) when a score passes it by
-// more than 2^64: weights up to 2^64 lose nothing in fp32 or bf16, and the usual tile
-// needs one vote per warp and no exchange of maxima. P is rounded to bf16 for
+// and is only raised (and O and the sums rescaled) when a score of the row passes
+// it by more than 2^8, as in the prefill: weights up to 2^8 lose nothing in fp32 or
+// bf16 and leave V all but the last 2^8 of its range, and the usual tile needs
+// one vote per warp and no exchange of maxima. P is rounded to bf16 for
 // the product; out is normalised by the sum of the rounded weights, lse
 // uses the unrounded sum.
 #pragma once
@@ -69,8 +70,8 @@ constexpr int EX_MAX_CTAS = 160;      // partial-result slots: two per CTA
 // Places that a launch's line has at most: calls whose shapes allow for more are
 // refused (malformed offsets can still make more; those are cut off).
 constexpr long long EX_MAX_TILES = 0x7fffffffll;
-constexpr float EX_RAISE_LOG2 = 64.0f;   // see the softmax above
-constexpr float EX_NO_MAX = -3.0e38f;    // reference of a row that saw no key yet
+constexpr float EX_RAISE_LOG2 = PF_RESCALE_LOG2;   // see the softmax above
+constexpr float EX_NO_MAX = -3.402823466e38f;      // reference of a row that saw no key yet
 
 // Places in the line of tiles that a unit takes besides its tiles: what its
 // start and end cost, in tiles (chunks of up to 32 tokens of 24 ragged
@@ -979,18 +980,38 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 l32[c] = make_float2(0.f, 0.f);
                 if constexpr (!C::ONES) lr[c] = make_float2(0.f, 0.f);
             }
-            float limit = EX_NO_MAX;  // scores above this raise the references
             if constexpr (!FIX) {
                 neg = s_ref + ((++refs & 1) * C::NWG + wg) * HC;
-                if (lane < HC) neg[lane] = -EX_NO_MAX;  // all four warps write the same
+                // all four warps write the same; rows that only fill the unit
+                // (products of 0) never ask for a raise
+                if (lane < HC) neg[lane] = wg * HC + lane < 2 * U.tvalid ? -EX_NO_MAX : 0.f;
                 __syncwarp();
             }
-            // Waits for tile t's scores and reads them; with a running reference
-            // also this warp's vote on raising it: its largest score (also of
-            // keys that a row does not see, which errs on the safe side) against
-            // the lowest reference of the warpgroup's rows.
+            // Scores in log2 units less their rows' references: rounded in between, as
+            // the references are, so that a row's largest score comes to 0 exactly
+            // whatever its size (fused, a score of 2^31 would be off by 2^6).
+            auto shift = [&](float (&x)[HC]) {
+#pragma unroll
+                for (int c = 0; c < HC; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(neg + c);
+                    const float2 by = make_float2(unit_l2, unit_l2);
+                    const float2 u =
+                        add2(mul2(make_float2(x[c], x[c + 1]), by), make_float2(f.x, f.y));
+                    const float2 v =
+                        add2(mul2(make_float2(x[c + 2], x[c + 3]), by), make_float2(f.z, f.w));
+                    x[c] = u.x;
+                    x[c + 1] = u.y;
+                    x[c + 2] = v.x;
+                    x[c + 3] = v.y;
+                }
+            };
+            // Waits for a tile's scores and reads them; with a running reference
+            // also shifts them by it and votes on raising it: whether a score
+            // (also of a key that its row does not see, which errs on the safe
+            // side) passes its row's reference by too much. A segment's first tile
+            // sets the references: its scores stay as they are.
             float next[HC];
-            auto peek = [&](int t, uint32_t it) -> bool {
+            auto peek = [&](bool first, uint32_t it) -> bool {
                 const uint32_t sb = it % EX_S_BUFS;
                 bool k = mbar_wait(&s_full[sb], (it / EX_S_BUFS) & 1, abort_flag, lim, SITE_EX_SM);
                 k = __all_sync(0xffffffffu, k);
@@ -998,16 +1019,14 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 tc_fence_after();
                 ex_scores<HC, FIX>(P, s_addr + sb * R, next);
                 if constexpr (!FIX) {
-                    float top = next[0], low = next[0];
+                    bool raise = true;
+                    if (!first) {
+                        shift(next);
+                        float top = next[0];
 #pragma unroll
-                    for (int c = 1; c + 1 < HC; c += 2) top = fmax3f(top, next[c], next[c + 1]);
-                    top = fmaxf(top, next[HC - 1]) * unit_l2;
-                    if (unit_l2 < 0.f) {
-#pragma unroll
-                        for (int c = 1; c < HC; ++c) low = fminf(low, next[c]);
-                        top = low * unit_l2;
+                        for (int c = 1; c + 1 < HC; c += 2) top = fmax3f(top, next[c], next[c + 1]);
+                        raise = __any_sync(0xffffffffu, fmaxf(top, next[HC - 1]) > EX_RAISE_LOG2);
                     }
-                    const bool raise = __any_sync(0xffffffffu, top > limit);
                     if (lane == 0) {
                         votes[((it & 1) * C::NWG + wg) * 4 + qd] = raise;
                         mbar_arrive(&wg_vote[wg]);
@@ -1029,7 +1048,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         p[c] = -INFINITY;
                 }
             };
-            ok = peek(t_begin, done);
+            ok = peek(true, done);
             for (int t = t_begin; t < t_end && ok; ++t) {
                 const uint32_t it = done + (t - t_begin);
                 const uint32_t b = it & 1;
@@ -1040,6 +1059,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                     // the same decision in the whole warpgroup
                     if (*reinterpret_cast<volatile uint32_t*>(votes + (b * C::NWG + wg) * 4) != 0) {
                         float* st = s_max + ((raises & 1) * C::NWG + wg) * 4 * HC;
+                        // without the shift
+                        if (t > t_begin) ex_scores<HC, FIX>(P, s_addr + (it % EX_S_BUFS) * R, next);
                         {
                             float mx[HC];
 #pragma unroll
@@ -1068,12 +1089,7 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                         }
                         neg = to;
                         __syncwarp();
-                        // the lowest reference, rows that only fill the unit aside
-                        limit = lane < HC && wg * HC + lane < 2 * U.tvalid ? -neg[lane] : INFINITY;
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            limit = fminf(limit, __shfl_xor_sync(0xffffffffu, limit, o));
-                        limit += EX_RAISE_LOG2;
+                        shift(next);
 #pragma unroll
                         for (int c = 0; c < HC / 2; ++c) {
                             const float fx = fac[pair_row(c, 0)], fy = fac[pair_row(c, 1)];
@@ -1109,27 +1125,11 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 }
                 float p[HC];
 #pragma unroll
-                for (int c = 0; c < HC; c += 4) {
-                    if constexpr (FIX) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) p[c + k] = next[c + k];
-                    } else {
-                        const float4 f = *reinterpret_cast<const float4*>(neg + c);
-                        const float2 by = make_float2(unit_l2, unit_l2);
-                        const float2 u =
-                            fma2(make_float2(next[c], next[c + 1]), by, make_float2(f.x, f.y));
-                        const float2 v =
-                            fma2(make_float2(next[c + 2], next[c + 3]), by, make_float2(f.z, f.w));
-                        p[c] = u.x;
-                        p[c + 1] = u.y;
-                        p[c + 2] = v.x;
-                        p[c + 3] = v.y;
-                    }
-                }
+                for (int c = 0; c < HC; ++c) p[c] = next[c];
                 mask(t, p);
                 // the next tile's scores (and vote) while this one's weights go out
                 if (t + 1 < t_end) {
-                    ok = peek(t + 1, it + 1);
+                    ok = peek(false, it + 1);
                     if (!ok) break;
                 }
 #pragma unroll

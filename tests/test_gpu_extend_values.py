@@ -184,3 +184,70 @@ def test_queries_before_the_first_key_beside_nan():
         assert torch.count_nonzero(out[:4]) == 0 and (lse[:, :4] == -INF).all()
         assert torch.isnan(out[4:6].float()).all() and torch.isnan(lse[:, 4:6]).all()
         assert torch.isfinite(out[6:].float()).all() and math.isfinite(float(lse[:, 6:].sum()))
+
+
+@pytest.mark.parametrize("cap", [0.0, 100.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(4, 700), (8, 600)] * 8, [(13, 900)] * 12, [(30, 1500)] * 8],
+                         ids=["4-8", "13", "30"])
+def test_values_of_any_size(lens, d, cap):
+    """Scores that rise by 2^40 along the cache with values 2^100 and 2^-100 of
+    the usual ones: as a weighted mean the result scales alike. (Weights that
+    were allowed to grow that far before they are rescaled would overflow. Many
+    units, so that a CTA meets a unit's tiles one after the other.)"""
+    c = Chunks(lens, d, cap, H=32, Hkv=16, seed=d + 2)
+    way = torch.sign(torch.randn(d, generator=torch.Generator().manual_seed(3)))
+    c.q.copy_((0.1 * c.q.float() + way).bfloat16())
+    for s, (T, S) in enumerate(lens):
+        rise = 28.0 / d ** 0.5 * torch.linspace(0.0, 1.0, S).clamp_min(0.2)[:, None, None]
+        rows = slice(int(c.ck[s]), int(c.ck[s]) + S)
+        c.k[rows] = (0.1 * c.k[rows].float() + rise * way).bfloat16()
+    ro, rl = c.oracle()
+    v = c.v.clone()
+    for power in (0, 100, -100):
+        c.v.copy_(v.float() * 2.0 ** power)
+        out, lse = c.run()
+        check(out * 2.0 ** -power, ro, lse, rl, f"{d} {cap} 2^{power}")
+
+
+@pytest.mark.parametrize("d,T", [(64, 3), (128, 12), (256, 30)])
+def test_lowest_scores(d, T):
+    """Without the cap, rows whose every score is near the lowest finite number
+    still are weighted means: equal scores, equal weights."""
+    c = Chunks([(T, 400), (1, 130)], d, 0.0, seed=4)
+    c.q.fill_(1.0)
+    # products of -2^127: -3.2e38 in log2 units, the lowest number is -3.4e38
+    c.k.fill_(-2.0 ** 127 / d)
+    c.kw["query_scale"] = 1.3
+    out, lse = c.run()
+    for s, (t, S) in enumerate([(T, 400), (1, 130)]):
+        for i in range(t):
+            j = slice(int(c.ck[s]), int(c.ck[s]) + S - t + i + 1)
+            want = c.v[j].double().mean(0).repeat_interleave(2, 0).numpy()
+            row = int(c.cq[s]) + i
+            check(out[row], want, what=f"{s} {i}")
+            assert torch.allclose(lse[:, row].double(),
+                                  torch.full((4,), -1.3 * 2.0 ** 127, dtype=torch.float64), rtol=1e-5)
+
+
+@pytest.mark.parametrize("d,lens", [(64, [(4, 700), (8, 600)] * 8), (128, [(13, 900)] * 12),
+                                    (256, [(30, 1500)] * 8)], ids=["64", "128", "256"])
+def test_nan_where_scores_rise(d, lens):
+    """A NaN row, and one before a NaN key, in units whose references are raised
+    tile by tile."""
+    c = Chunks(lens, d, 0.0, H=32, Hkv=16, seed=d + 5)
+    way = torch.sign(torch.randn(d, generator=torch.Generator().manual_seed(3)))
+    c.q.copy_((0.1 * c.q.float() + way).bfloat16())
+    for s, (T, S) in enumerate(lens):
+        rise = 60.0 / d ** 0.5 * torch.linspace(0.0, 1.0, S)[:, None, None]
+        rows = slice(int(c.ck[s]), int(c.ck[s]) + S)
+        c.k[rows] = (0.1 * c.k[rows].float() + rise * way).bfloat16()
+    ro, rl = c.oracle()
+    bad = np.zeros((c.q.shape[0], c.H), dtype=bool)
+    for s, (T, S) in enumerate(lens):
+        row, h, g = int(c.cq[s]) + s % T, (5 * s) % c.H, (3 * s) % 16
+        c.q[row, h, s] = NAN
+        bad[row, h] = True
+        c.k[int(c.ck[s]) + S - 2, g, s] = NAN
+        bad[:, 2 * g:2 * g + 2] |= c.sees(s, S - 2)[:, None]
+    held(*c.run(), ro, rl, bad, f"{d}")
