@@ -27,6 +27,7 @@ first call raises.
 from __future__ import annotations
 
 import ctypes
+import decimal
 import functools
 import math
 import os
@@ -579,6 +580,43 @@ class RopePlan(NamedTuple):
     mscale: float = 1.0
 
 
+# Digits that the tables are made with: 64-bit fixed point of a turn per position
+# wants 20, and what positions of 31 bits multiply must be right behind them.
+_DIGITS = decimal.Context(prec=60)
+_TWO_PI = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def _rope_radians(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained_len=8192,
+                  fast_turns=32.0, slow_turns=1.0):
+    """:func:`rope_frequencies` in decimal numbers of 60 digits."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    half, mscale = rotary_dim // 2, 1.0
+    num = decimal.Decimal
+    with decimal.localcontext(_DIGITS):
+        wide, times = num(float(base)), num(float(factor))
+        if scaling == "ntk" and rotary_dim > 2:
+            wide *= times ** (num(rotary_dim) / (rotary_dim - 2))
+        inv = [wide ** (num(-2 * i) / rotary_dim) for i in range(half)]
+        if scaling == "linear":
+            inv = [w / times for w in inv]
+        elif scaling == "yarn":
+            def pair(turns):  # the (fractional) pair that turns so often over trained_len
+                return (rotary_dim * math.log(trained_len / (turns * 2.0 * math.pi))
+                        / (2.0 * math.log(base)))
+            low = max(math.floor(pair(fast_turns)), 0)
+            high = min(math.ceil(pair(slow_turns)), rotary_dim - 1)
+            ramp = [min(max(num(i - low) / max(num(high - low), num("0.001")), num(0)), num(1))
+                    for i in range(half)]
+            inv = [w / times * r + w * (1 - r) for w, r in zip(inv, ramp)]
+            mscale = 0.1 * math.log(factor) + 1.0
+    return inv, mscale
+
+
 def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained_len=8192,
                      fast_turns=32.0, slow_turns=1.0):
     """Radians per position of every pair, and the factor on the rotation.
@@ -590,44 +628,30 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
     those that turn more than ``fast_turns`` times, a ramp between, and the
     rotation times 0.1 ln(factor) + 1.
     """
-    if rotary_dim < 2 or rotary_dim % 2:
-        raise ValueError("rotary_dim must be even and positive")
-    if not base > 1.0 or not factor >= 1.0:
-        raise ValueError("base must be above 1 and factor at least 1")
-    half, mscale = rotary_dim // 2, 1.0
-    if scaling == "ntk" and rotary_dim > 2:
-        base = base * factor ** (rotary_dim / (rotary_dim - 2))
-    inv = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
-    if scaling == "linear":
-        inv = [w / factor for w in inv]
-    elif scaling == "yarn":
-        def pair(turns):  # the (fractional) pair that turns so often over trained_len
-            return (rotary_dim * math.log(trained_len / (turns * 2.0 * math.pi))
-                    / (2.0 * math.log(base)))
-        low = max(math.floor(pair(fast_turns)), 0)
-        high = min(math.ceil(pair(slow_turns)), rotary_dim - 1)
-        ramp = [min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(half)]
-        inv = [w / factor * r + w * (1.0 - r) for w, r in zip(inv, ramp)]
-        mscale = 0.1 * math.log(factor) + 1.0
-    elif scaling not in (None, "ntk"):
-        raise ValueError(f"unknown scaling {scaling!r}")
-    return inv, mscale
+    inv, mscale = _rope_radians(rotary_dim, base, scaling, factor, trained_len, fast_turns,
+                                slow_turns)
+    return [float(w) for w in inv], mscale
 
 
 def rope_plan(rotary_dim, *, interleaved=False, device="cuda", frequencies=None, mscale=None,
               **scaling):
-    """A :class:`RopePlan` on ``device`` from :func:`rope_frequencies` (whose
-    arguments ``scaling`` are) or from ``frequencies`` (radians per position)."""
+    """A :class:`RopePlan` on ``device`` from the arguments of
+    :func:`rope_frequencies` (``scaling``), or from ``frequencies`` (radians per
+    position, as doubles). The table holds their turns per position rounded once,
+    to 2^-65: phases of any int32 position are right to 2^-34 turns."""
     if torch is None:
         _load_torch()
     m = 1.0
     if frequencies is None:
-        frequencies, m = rope_frequencies(rotary_dim, **scaling)
+        frequencies, m = _rope_radians(rotary_dim, **scaling)
     elif scaling:
         raise ValueError("give frequencies or their parameters, not both")
+    else:
+        frequencies = [decimal.Decimal(float(w)) for w in frequencies]
     if len(frequencies) != rotary_dim // 2:
         raise ValueError("one frequency per pair")
-    turns = [round(w / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for w in frequencies]
+    with decimal.localcontext(_DIGITS):
+        turns = [int((w / _TWO_PI * 2 ** 64).to_integral_value()) % 2 ** 64 for w in frequencies]
     freqs = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64,
                          device=device)
     return RopePlan(freqs, int(rotary_dim), bool(interleaved), m if mscale is None else mscale)
