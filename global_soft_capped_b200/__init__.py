@@ -962,7 +962,10 @@ def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, copies=Fal
     granted (num_seqs,) int32, 0 where the pages ran out. A sequence that was cut
     (:func:`pages_truncate`) inside a page which a fork shares needs a copy of it:
     with ``copies`` the result is (granted, copy_src, copy_dst) for
-    :func:`pages_copy`, without it such a sequence is refused."""
+    :func:`pages_copy`, without it such a sequence is refused. Each of several
+    sequences that share such a page and grow in one call gets a copy. Issue the
+    copies before the next grow, fork or compact, and not together with theirs:
+    the pages read may count as free by now."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     ws, wp, wb = _pages_ws(workspace, stream, block_table, n, nb)
@@ -991,7 +994,8 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
                stream=None):
     """Every sequence s a fork of sequence parents[s] (s: stays). ref_counts in
     place; returns (block_table, seq_lens, copy_src, copy_dst, granted), the
-    first two new. Copy the pages (:func:`pages_copy`) before appending."""
+    first two new. Copy the pages (:func:`pages_copy`) before appending and before
+    the next grow, fork or compact, as those of :func:`pages_grow`."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     table = _new(stream, torch.empty_like, block_table)
@@ -1006,7 +1010,8 @@ def pages_fork(block_table, seq_lens, ref_counts, parents, block_size, *, worksp
 
 def pages_compact(block_table, ref_counts, *, workspace=None, stream=None):
     """Renumbers the live pages to the front of the cache, in place; returns
-    (copy_src, copy_dst, num_live) for :func:`pages_copy`."""
+    (copy_src, copy_dst, num_live) for :func:`pages_copy`, to be issued before
+    anything reads the caches and before the next grow, fork or compact."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     src, dst = _new(stream, block_table.new_empty, (2, nb // 2)).unbind(0)

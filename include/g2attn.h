@@ -453,6 +453,12 @@ G2ATTN_API int g2attn_extend_paged(const void* q, const void* k_blocks, const vo
  *   aligned, no initial contents needed, not shared by calls that may overlap.
  * Nothing outside the arrays is touched, whatever they hold. Calls on one set
  * of tables are ordered by the caller (one stream).
+ *   Pages to copy: grow, fork and compact say which pages the caller has to copy
+ *   (g2attn_pages_copy). The counts already are those after the copy, so a page
+ *   that is still to be read from may count as free. Each call's copies are
+ *   therefore issued before the next grow, fork or compact on these tables, which
+ *   could hand such a page out, in a g2attn_pages_copy of their own: pairs of
+ *   two calls in one copy could write a page that another pair of it reads.
  */
 G2ATTN_API size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks);
 
@@ -465,6 +471,9 @@ G2ATTN_API size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks);
  * caller copies (g2attn_pages_copy) from copy_src[s] to copy_dst[s] before it
  * appends (device int32 [num_seqs], -1: nothing to copy). Both may be NULL where
  * that cannot happen (no truncate below a fork); such a sequence is then refused.
+ * Shared is what the counts before the call say: when all sequences that share
+ * such a page grow in one call, each of them asks for a copy, one page more than
+ * the least, and the page itself is free afterwards.
  */
 G2ATTN_API int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
                       int* granted, int* copy_src, int* copy_dst, int num_seqs, int num_blocks, int block_size,
