@@ -823,7 +823,9 @@ def _append(q, k, v, cu_seqlens_q, num_seqs, q_out, stream):
 def rope_append(q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, plan, *, q_out=None,
                 stream=None):
     """Rotates q (returned) and k and writes k and v to the last rows of every
-    sequence of a packed cache (sum L,Hkv,d); cu_seqlens_q None: one token each."""
+    sequence of a packed cache (sum L,Hkv,d); cu_seqlens_q None: one token each.
+    The lengths are those with the new tokens (with an older one the tokens
+    would overwrite the sequence's last rows)."""
     n_seqs = cu_seqlens_k.numel() - 1
     n, H, Hkv, d, qs, ks, vs, q_out, cu = _append(q, k, v, cu_seqlens_q, n_seqs, q_out, stream)
     kc, vc = _cache("k_cache", k_cache, 3, Hkv, d, q.device), _like_cache("v_cache", v_cache, k_cache)
@@ -965,7 +967,8 @@ def pages_grow(block_table, seq_lens, ref_counts, add, block_size, *, copies=Fal
     :func:`pages_copy`, without it such a sequence is refused. Each of several
     sequences that share such a page and grow in one call gets a copy. Issue the
     copies before the next grow, fork or compact, and not together with theirs:
-    the pages read may count as free by now."""
+    the pages read may count as free by now. A refused sequence keeps its length:
+    give the appends none of its tokens, they would overwrite its last rows."""
     tp, n, cols, nb, rp = _table(block_table, ref_counts)
     dev = block_table.device
     ws, wp, wb = _pages_ws(workspace, stream, block_table, n, nb)

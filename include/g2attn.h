@@ -356,6 +356,10 @@ G2ATTN_API int g2attn_rope(const void* q, const void* k, void* q_out, void* k_ou
  *   A token that has no row in its cache (T_s > L_s, lengths past the cache)
  *   writes nothing to it, and g2attn_get_device_error reports
  *   G2ATTN_ERR_CACHE_ROW. Nothing outside the tensors is touched.
+ *   The lengths must be those with the new tokens already. With the old length
+ *   (a sequence that g2attn_pages_grow refused) the tokens would overwrite its
+ *   last T_s rows, which exist, so nothing would be reported: leave such a
+ *   sequence out (T_s = 0; with one token each, length 0).
  */
 G2ATTN_API int g2attn_rope_append(const void* q, const void* k, const void* v, void* q_out,
                        void* k_cache, void* v_cache, const int* cu_seqlens_q,
@@ -474,6 +478,8 @@ G2ATTN_API size_t g2attn_pages_workspace_size(int num_seqs, int num_blocks);
  * Shared is what the counts before the call say: when all sequences that share
  * such a page grow in one call, each of them asks for a copy, one page more than
  * the least, and the page itself is free afterwards.
+ * A refused sequence keeps its old length and must sit the append out (see
+ * g2attn_rope_append).
  */
 G2ATTN_API int g2attn_pages_grow(int* block_table, int* seq_lens, int* ref_counts, const int* add,
                       int* granted, int* copy_src, int* copy_dst, int num_seqs, int num_blocks, int block_size,
