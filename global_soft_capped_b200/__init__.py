@@ -591,6 +591,7 @@ def _rope_radians(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained_le
     """:func:`rope_frequencies` in decimal numbers of 60 digits."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive")
+    rotary_dim = int(rotary_dim)  # (of a numpy integer, too)
     if not base > 1.0 or not factor >= 1.0:
         raise ValueError("base must be above 1 and factor at least 1")
     if scaling not in (None, "linear", "ntk", "yarn"):

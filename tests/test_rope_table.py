@@ -93,3 +93,18 @@ def test_table_and_frequencies_agree(scaling):
     for f, w in zip(table(plan), inv):
         assert abs(Fraction(f, 2 ** 64) - Fraction(w) / (2 * PI)) <= Fraction(w) * 2 / 2 ** 54 + \
             Fraction(1, 2 ** 64)
+
+
+def test_numbers_of_any_kind():
+    """numpy and torch scalars, as sizes read from a configuration may be."""
+    import numpy as np
+    import torch
+    want = g2.rope_plan(64, device="cpu", base=500000.0, scaling="ntk", factor=4.0)
+    for n, b, f in ((np.int64(64), np.float32(500000), np.float64(4)),
+                    (64, torch.tensor(500000.0), 4)):
+        got = g2.rope_plan(n, device="cpu", base=b, scaling="ntk", factor=f)
+        assert torch.equal(got.freqs, want.freqs) and got.rotary_dim == 64
+    inv, _ = g2.rope_frequencies(np.int32(8), scaling="yarn", factor=np.float32(2))
+    assert inv == g2.rope_frequencies(8, scaling="yarn", factor=2.0)[0]
+    given = g2.rope_plan(np.int64(4), device="cpu", frequencies=np.array([1.0, 0.5]))
+    assert torch.equal(given.freqs, g2.rope_plan(4, device="cpu", frequencies=[1.0, 0.5]).freqs)
