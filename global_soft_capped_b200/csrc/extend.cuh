@@ -74,9 +74,14 @@ constexpr float EX_RAISE_LOG2 = PF_RESCALE_LOG2;   // see the softmax above
 constexpr float EX_NO_MAX = -3.402823466e38f;      // reference of a row that saw no key yet
 
 // Places in the line of tiles that a unit takes besides its tiles: what its
-// start and end cost, in tiles (chunks of up to 32 tokens of 24 ragged
-// sequences, d = 128: 288 us without, 259 with 2, 238 with 4, 235 with 6)
-constexpr int ex_unit_cost(int d) { return 768 / d; }
+// start and end cost, in tiles (a tile's time goes with d, a unit's end much less).
+// Over 54 shapes (d = 64, 128, 256; 4, 9-16, 17-32 tokens; 64 to 8,192 keys;
+// with and without the cap) the times of 0, 384 / d and 768 / d to those of 512 / d
+// are 1.08, 0.99 and 1.02 in the mean; 384 / d is slower for long chunks (24
+// sequences of 1,000 to 16,000 keys, 17-32 tokens, d = 128, uncapped: 252 us
+// against 244; d = 256, 500 to 8,192 keys: 177 against 172), 768 / d for short
+// ones (4 tokens, 200 to 2,000 keys, d = 128: 72 against 69).
+constexpr int ex_unit_cost(int d) { return 512 / d; }
 
 template <int D, int R>
 struct ExCfg {
