@@ -602,9 +602,10 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
         static_assert(RL == 2, "rows or the seen range");
         // 32 entries of the sequence's table from page `w_page` on, one per lane,
         // and the 32 after them, loaded long before they are needed: loading a
-        // tile's entries while the tile before it loads left most of their
-        // latency in the producers' way (30,001 keys in pages of 16, d = 256:
-        // 33.3 us against 30.9; 64 sequences of 500 keys, d = 128: 62 against 54).
+        // tile's entries when it comes up leaves most of their latency in the
+        // producers' way (32 ragged sequences of 500 to 8,192 keys in pages of 16,
+        // 16 KV heads, d = 128, 1-8 tokens: 218 us against 207, 9-16 tokens: 203
+        // against 193; one sequence of 30,001 keys, d = 256: 32.9 against 32.4).
         int w_seq = -1, w_page = 0, w_now = 0, w_next = 0;
         auto entry_of = [&](int seq, int page) -> int {
             return page < P.max_blocks ? P.table[static_cast<size_t>(seq) * P.max_blocks + page] : 0;
@@ -638,8 +639,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                 const int key = k0 + box * P.box_rows, end = key + P.box_rows;
                 const int e =
                     __shfl_sync(0xffffffffu, w_now, ((key >> P.block_shift) - w_page) & 31);
-                // the usual tile (without this short cut the uncapped 32-token chunks
-                // of 24 sequences take 251 us instead of 247)
+                // the usual tile (without this short cut 24 ragged sequences of 500 to
+                // 8,192 keys, 17-32 tokens, d = 128, take 185 us instead of 180)
                 if (k0 >= U.lo && k0 + EX_BN <= U.hi) {
                     T.row = cache_row(e, key);
                     return;
@@ -676,7 +677,8 @@ __global__ void __launch_bounds__(ExCfg<D, R>::THREADS, 1) extend_sm100(
                                                        (C::SLOT_COLS * 2));
                 // a 64-column chunk per warp, or every other box: a copy takes its
                 // warp some 90 cycles to issue, 16 of them a slot at pages of 16
-                // (the whole slot by warp 0: 63 instead of 54 us in the case above)
+                // (the whole slot by warp 0: 64 sequences of 500 keys, 4 tokens, d = 128,
+                // take 69 us instead of 57)
                 const int chunk = C::NCH == 2 ? pw : 0;
                 if (lane < per_chunk && ((T.parts >> lane) & 1) == 0 &&
                     (C::NCH == 2 || (lane & 1) == pw))
