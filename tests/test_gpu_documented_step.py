@@ -1,4 +1,4 @@
-"""The decode step over a paged cache as README.md gives it, run as it stands
+"""The decode step over a paged cache that users are shown first, run as it stands
 there: sequences that are refused rows, or share a page they were cut in."""
 import os
 import re
